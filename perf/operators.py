@@ -197,8 +197,10 @@ def _plain_quant(x):
 
 
 def _fp8(x):
-    """Per-row FP8: the codes' values and the scale."""
-    s = x.abs().amax(-1, keepdim=True) / 448.0
+    """Per-row FP8: the codes' values and the scale (divided by a tensor: by a number, torch multiplies with its
+    rounded reciprocal)."""
+    s = x.abs().amax(-1, keepdim=True)
+    s = s / torch.full_like(s, 448.0)
     q = torch.where(s > 0, x / s, torch.zeros_like(x)).to(torch.float8_e4m3fn).float()
     return q, s
 
@@ -269,7 +271,8 @@ def _exact_e4m3(x):
     """x rounded to E4M3 (3 mantissa bits, smallest step 2^-9, at most 448), scaled by its row's maximum.  Both
     divisions are the definition's own, in the type of x: hidden states are bf16 numbers, whose quotients fall on the
     border between two codes often enough that their rounding in fp32 is part of the definition."""
-    s = x.abs().max() / 448
+    s = x.abs().max(0, keepdim=True).values
+    s = s / torch.full_like(s, 448)
     if s == 0:
         return torch.zeros_like(x).double(), s.double()
     y, s = (x / s).double(), s.double()

@@ -74,6 +74,15 @@ class _CLayerH(ctypes.Structure):
                 ("sh_down", ctypes.c_void_p)]
 
 
+class _CLayerMX(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int), ("H", ctypes.c_int), ("N", ctypes.c_int),
+                ("gate_f4", ctypes.c_void_p), ("up_f4", ctypes.c_void_p), ("down_f4", ctypes.c_void_p),
+                ("gate_e8", ctypes.c_void_p), ("up_e8", ctypes.c_void_p), ("down_e8", ctypes.c_void_p),
+                ("n_shared", ctypes.c_int), ("shared_N", ctypes.c_int),
+                ("sh_gate", ctypes.c_void_p), ("sh_up", ctypes.c_void_p),
+                ("sh_down", ctypes.c_void_p)]
+
+
 class _CLayout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in
                 ("topk_ids", "topk_w", "expert_offsets", "sorted_pairs", "row_of_pair",
@@ -145,6 +154,14 @@ def lib() -> ctypes.CDLL:
         L.moe_ep_experts_workspace_bytes.restype = sz
         L.moe_ep_experts_forward.argtypes = [ctypes.POINTER(_CLayer), vp, i64, vp, vp, sz, vp]
         L.moe_ep_combine.argtypes = [ctypes.POINTER(_CLayer), vp, vp, i64, i32, vp, vp, sz, vp]
+        L.mxfp4_quant_rows.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+        L.mxfp4_dequant_rows.argtypes = [vp, vp, i64, i64, vp, i32, vp]
+        L.mxfp4_matmul.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, i32, vp]
+        for name, struct in (("w4a8", _CLayer), ("mxfp4", _CLayerMX)):
+            size = getattr(L, f"moe_{name}_decode_workspace_bytes")
+            size.argtypes, size.restype = [ctypes.POINTER(struct), i64, i32], sz
+            for tail in ("decode", "decode_router"):
+                getattr(L, f"moe_{name}_{tail}").argtypes = [ctypes.POINTER(struct), vp, vp, i64, i32, vp, vp, sz, vp]
         L.moe_last_device_status.argtypes = [vp]
         L.moe_selftest_bounded_wait.argtypes = [i64, vp]
         L.moe_status_string.argtypes = [i32]
@@ -661,3 +678,154 @@ def moe_hybrid_forward_profiled(layer: LayerH, x, logits, k: int, out, ws, event
                                              _ptr(ws), nbytes, _stream(stream), arr, len(events),
                                              ctypes.byref(n)), "moe_hybrid_forward_profiled")
     return int(n.value)
+
+
+# ---- MXFP4 rows and experts ---------------------------------------------------------------------
+
+def _dtype_code(dtype) -> int:
+    """moe_dtype of a torch dtype."""
+    import torch
+    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(dtype)
+    if code is None:
+        raise ValueError(f"expected bfloat16, float16 or float32, got {dtype}")
+    return code
+
+
+def _want(t, name: str, dtype, *shape):
+    """The tensor's device pointer, once its type, shape, device and layout are as the call reads it."""
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    return _here(t, name)
+
+
+def _here(t, name: str):
+    import torch
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: expected a tensor on the current CUDA device, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def mxfp4_quant_rows(x, codes, scales, stream=None) -> None:
+    """x bf16 / f16 / fp32 [rows, K] (rows may be strided) -> codes uint8 [rows, K/2], E8M0 scales
+    uint8 [rows, K/32]."""
+    import torch
+    rows, K = x.shape
+    if x.stride(1) != 1 and K > 1:
+        raise ValueError("x: expected rows with consecutive columns")
+    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
+        raise ValueError(f"x: expected a tensor on the current CUDA device, got {x.device}")
+    _check(lib().mxfp4_quant_rows(x.data_ptr(), _dtype_code(x.dtype), rows, K, x.stride(0),
+                                  _want(codes, "codes", torch.uint8, rows, K // 2),
+                                  _want(scales, "scales", torch.uint8, rows, K // 32),
+                                  _stream(stream)), "mxfp4_quant_rows")
+
+
+def mxfp4_dequant_rows(codes, scales, y, stream=None) -> None:
+    """codes uint8 [rows, K/2], scales uint8 [rows, K/32] -> y bf16 / fp32 [rows, K]."""
+    import torch
+    rows, K = y.shape
+    _check(lib().mxfp4_dequant_rows(_want(codes, "codes", torch.uint8, rows, K // 2),
+                                    _want(scales, "scales", torch.uint8, rows, K // 32), rows, K, _here(y, "y"),
+                                    _dtype_code(y.dtype), _stream(stream)), "mxfp4_dequant_rows")
+
+
+def mxfp4_matmul(a, a_scales, b, b_scales, out, stream=None) -> None:
+    """out bf16 / fp32 [M, N] = A B^T over MXFP4 rows a uint8 [M, K/2], b uint8 [N, K/2]."""
+    import torch
+    M, N, K = a.shape[0], b.shape[0], 2 * a.shape[1]
+    u8 = torch.uint8
+    _check(lib().mxfp4_matmul(_want(a, "a", u8, M, K // 2), _want(a_scales, "a_scales", u8, M, K // 32),
+                              _want(b, "b", u8, N, K // 2), _want(b_scales, "b_scales", u8, N, K // 32), M, N, K,
+                              _want(out, "out", out.dtype, M, N), _dtype_code(out.dtype), _stream(stream)),
+           "mxfp4_matmul")
+
+
+@dataclass
+class LayerMX:
+    """Device tensors of one layer with MXFP4 experts (moe_mxfp4_layer)."""
+    E: int
+    H: int
+    N: int
+    gate_f4: object
+    up_f4: object
+    down_f4: object
+    gate_e8: object
+    up_e8: object
+    down_e8: object
+    sh_gate: object = None
+    sh_up: object = None
+    sh_down: object = None
+
+    @property
+    def n_shared(self) -> int:
+        return 0 if self.sh_gate is None else int(self.sh_gate.shape[0])
+
+    @property
+    def shared_N(self) -> int:
+        return 0 if self.sh_gate is None else int(self.sh_gate.shape[1])
+
+    def c_struct(self) -> _CLayerMX:
+        return _CLayerMX(self.E, self.H, self.N, _ptr(self.gate_f4), _ptr(self.up_f4), _ptr(self.down_f4),
+                         _ptr(self.gate_e8), _ptr(self.up_e8), _ptr(self.down_e8),
+                         self.n_shared, self.shared_N, _ptr(self.sh_gate), _ptr(self.sh_up),
+                         _ptr(self.sh_down))
+
+    def shape_struct(self) -> _CLayerMX:
+        return _CLayerMX(self.E, self.H, self.N, None, None, None, None, None, None,
+                         self.n_shared, self.shared_N, None, None, None)
+
+
+def layermx_struct(E, H, N, n_shared=0, shared_N=0) -> _CLayerMX:
+    return _CLayerMX(E, H, N, None, None, None, None, None, None, n_shared, shared_N, None, None, None)
+
+
+# ---- the layer for a few tokens -----------------------------------------------------------------
+
+def moe_w4a8_decode_workspace_bytes(layer, T: int, k: int) -> int:
+    s = layer if isinstance(layer, _CLayer) else layer.shape_struct()
+    return int(lib().moe_w4a8_decode_workspace_bytes(ctypes.byref(s), T, k))
+
+
+def moe_mxfp4_decode_workspace_bytes(layer, T: int, k: int) -> int:
+    s = layer if isinstance(layer, _CLayerMX) else layer.shape_struct()
+    return int(lib().moe_mxfp4_decode_workspace_bytes(ctypes.byref(s), T, k))
+
+
+def _decode(fn, where: str, layer, x, routing, routing_dtype, routing_rows, k, out, ws, stream):
+    import torch
+    T, H = x.shape[0], layer.H
+    s = layer.c_struct()
+    _check(fn(ctypes.byref(s), _want(x, "x", torch.bfloat16, T, H),
+              _want(routing, "routing", routing_dtype, *routing_rows), T, k,
+              _want(out, "out", torch.bfloat16, T, H), _here(ws, "ws"), ws.numel() * ws.element_size(),
+              _stream(stream)), where)
+
+
+def moe_w4a8_decode(layer: Layer, x, logits, k: int, out, ws, stream=None) -> None:
+    """out bf16 [T, H] = the W4A8 layer (+ shared experts) on x bf16 [T <= 16, H], logits fp32 [T, E]."""
+    import torch
+    _decode(lib().moe_w4a8_decode, "moe_w4a8_decode", layer, x, logits, torch.float32, (x.shape[0], layer.E), k, out,
+            ws, stream)
+
+
+def moe_w4a8_decode_router(layer: Layer, x, wr, k: int, out, ws, stream=None) -> None:
+    """moe_w4a8_decode fed by the router weight wr bf16 [E, H]."""
+    import torch
+    _decode(lib().moe_w4a8_decode_router, "moe_w4a8_decode_router", layer, x, wr, torch.bfloat16,
+            (layer.E, layer.H), k, out, ws, stream)
+
+
+def moe_mxfp4_decode(layer: LayerMX, x, logits, k: int, out, ws, stream=None) -> None:
+    """out bf16 [T, H] = the layer with MXFP4 experts on x bf16 [T <= 16, H], logits fp32 [T, E]."""
+    import torch
+    _decode(lib().moe_mxfp4_decode, "moe_mxfp4_decode", layer, x, logits, torch.float32, (x.shape[0], layer.E), k, out,
+            ws, stream)
+
+
+def moe_mxfp4_decode_router(layer: LayerMX, x, wr, k: int, out, ws, stream=None) -> None:
+    """moe_mxfp4_decode fed by the router weight wr bf16 [E, H]."""
+    import torch
+    _decode(lib().moe_mxfp4_decode_router, "moe_mxfp4_decode_router", layer, x, wr, torch.bfloat16,
+            (layer.E, layer.H), k, out, ws, stream)

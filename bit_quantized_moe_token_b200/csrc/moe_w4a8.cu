@@ -22,6 +22,9 @@ __device__ int g_device_status = 0;
 #include "route.cuh"
 #include "forward.cuh"
 #include "ep.cuh"
+#include "mxfp4.cuh"
+#include "mxfp4_matmul.cuh"
+#include "decode.cuh"
 #include "router.cuh"
 #include "tc_ptx.cuh"
 

@@ -1,10 +1,13 @@
 """Convenience wrappers: torch allocation around the C entry points."""
 from __future__ import annotations
 
-from ._binding import (Layer, Layer4, Layer8, LayerH, moe_hybrid_forward, moe_hybrid_workspace_bytes,
+from ._binding import (Layer, Layer4, Layer8, LayerH, LayerMX, moe_hybrid_forward, moe_hybrid_workspace_bytes,
+                       moe_mxfp4_decode, moe_mxfp4_decode_router, moe_mxfp4_decode_workspace_bytes,
                        moe_nvfp4_forward, moe_nvfp4_workspace_bytes,
+                       moe_w4a8_decode, moe_w4a8_decode_router, moe_w4a8_decode_workspace_bytes,
                        moe_w4a8_forward, moe_w4a8_workspace_bytes, moe_w8a8_forward,
-                       moe_w8a8_workspace_bytes, nvfp4_quant_weights, w4a8_pack_weights,
+                       moe_w8a8_workspace_bytes, mxfp4_dequant_rows, mxfp4_matmul, mxfp4_quant_rows,
+                       nvfp4_quant_weights, w4a8_pack_weights,
                        w8a8_quant_weights)
 
 
@@ -125,4 +128,80 @@ def forward(layer, x, logits, k: int, out=None, ws=None, stream=None):
         moe_nvfp4_forward(layer, x, logits, k, out, ws, stream=stream)
     else:
         moe_w4a8_forward(layer, x, logits, k, out, ws, stream=stream)
+    return out
+
+
+def quant_mxfp4(x, stream=None):
+    """bf16, f16 or fp32 values [..., K] on the GPU -> (E2M1 codes uint8 [..., K/2], E8M0 scales
+    uint8 [..., K/32]).  Two-dimensional x may have strided rows."""
+    import torch
+    *lead, K = x.shape
+    if K % 32:
+        raise ValueError("K must be a multiple of 32")
+    rows = x if x.dim() == 2 else x.reshape(-1, K)
+    codes = torch.empty(*lead, K // 2, dtype=torch.uint8, device=x.device)
+    scales = torch.empty(*lead, K // 32, dtype=torch.uint8, device=x.device)
+    mxfp4_quant_rows(rows, codes.view(-1, K // 2), scales.view(-1, K // 32), stream=stream)
+    return codes, scales
+
+
+def dequant_mxfp4(codes, scales, dtype=None, stream=None):
+    """The values [..., K] of MXFP4 codes [..., K/2] and scales [..., K/32], bf16 (the default) or
+    fp32, both exact."""
+    import torch
+    *lead, half = codes.shape
+    y = torch.empty(*lead, 2 * half, dtype=dtype or torch.bfloat16, device=codes.device)
+    mxfp4_dequant_rows(codes.view(-1, half), scales.view(-1, half // 16), y.view(-1, 2 * half), stream=stream)
+    return y
+
+
+def matmul_mxfp4(a, a_scales, b, b_scales, dtype=None, out=None, stream=None):
+    """A B^T [M, N] of MXFP4 rows A [M, K] and B [N, K], as bf16 (the default) or fp32."""
+    import torch
+    if out is None:
+        out = torch.empty(a.shape[0], b.shape[0], dtype=dtype or torch.bfloat16, device=a.device)
+    mxfp4_matmul(a, a_scales, b, b_scales, out, stream=stream)
+    return out
+
+
+def make_layer_mxfp4(gate_w, up_w, down_w, sh_gate=None, sh_up=None, sh_down=None,
+                     stream=None) -> LayerMX:
+    """MXFP4-quantize bf16 expert weights gate/up [E, N, H], down [E, H, N]."""
+    E, N, H = gate_w.shape
+    g, u, d = (quant_mxfp4(w, stream=stream) for w in (gate_w, up_w, down_w))
+    return LayerMX(E, H, N, g[0], u[0], d[0], g[1], u[1], d[1], sh_gate=sh_gate, sh_up=sh_up, sh_down=sh_down)
+
+
+def alloc_decode_workspace(layer, T: int, k: int, device=None):
+    """Scratch for decode / decode_router on a W4A8 or MXFP4 layer."""
+    import torch
+    if isinstance(layer, LayerMX):
+        n, ref = moe_mxfp4_decode_workspace_bytes(layer, T, k), layer.gate_f4
+    else:
+        n, ref = moe_w4a8_decode_workspace_bytes(layer, T, k), layer.gate_packed
+    if n == 0 and T > 0:
+        raise ValueError("unsupported layer shape or token count for the few-token layer")
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device if device is not None else ref.device)
+
+
+def decode(layer, x, logits, k: int, out=None, ws=None, stream=None):
+    """The whole layer on up to 16 tokens (Layer: W4A8, LayerMX: MXFP4) from router logits [T, E]."""
+    import torch
+    if out is None:
+        out = torch.empty_like(x)
+    if ws is None:
+        ws = alloc_decode_workspace(layer, x.shape[0], k, x.device)
+    (moe_mxfp4_decode if isinstance(layer, LayerMX) else moe_w4a8_decode)(layer, x, logits, k, out, ws, stream=stream)
+    return out
+
+
+def decode_router(layer, x, wr, k: int, out=None, ws=None, stream=None):
+    """decode() with the logits computed from the router weight wr [E, H]."""
+    import torch
+    if out is None:
+        out = torch.empty_like(x)
+    if ws is None:
+        ws = alloc_decode_workspace(layer, x.shape[0], k, x.device)
+    fn = moe_mxfp4_decode_router if isinstance(layer, LayerMX) else moe_w4a8_decode_router
+    fn(layer, x, wr, k, out, ws, stream=stream)
     return out

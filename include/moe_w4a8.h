@@ -487,6 +487,87 @@ int moe_ep_combine(const moe_w4a8_layer* layer, const uint16_t* x_bf16, const fl
                    int64_t T, int k, uint16_t* out_bf16, void* ws, size_t ws_bytes,
                    moe_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------
+ * MXFP4 rows: quantization, values and product.
+ *
+ * The OCP microscaling format MXFP4 (OCP Microscaling Formats (MX) Specification v1.0): K in
+ * blocks of 32, one E8M0 scale 2^(b - 127) a block (b = 255: NaN) and E2M1 codes, two a byte with
+ * the first in the low nibble (the code values of the NVFP4 section above).
+ *
+ * mxfp4_quant_rows, for each block of 32 values x:
+ *     b    = clamp(floor(log2 max|x|) + 125, 0, 254)
+ *     code = E2M1 value nearest to x / 2^(b - 127), ties to the even code, at most +-6, sign kept
+ * (the specification's conversion, section 6.3); a block of zeros gets b = 0, a block that holds a
+ * NaN or an infinity gets b = 255 and codes 0 and reads back as NaN.
+ *   x           [rows, K] of type x_type, rows `row_stride` elements apart (>= K; ignored for one
+ *               row); x and row_stride in bytes multiples of 16
+ *   K           a positive multiple of 32
+ *   codes       [rows, K/2] out, 4-byte aligned        scales  [rows, K/32] out
+ * mxfp4_dequant_rows: y [rows, K] of type MOE_BF16 or MOE_F32, 16-byte aligned, every value exact.
+ * rows == 0 is a no-op.  Return MOE_OK, MOE_ERR_INVALID_ARG (null pointer, negative size, unknown
+ * type, stride below K), MOE_ERR_UNSUPPORTED_SHAPE, MOE_ERR_MISALIGNED or MOE_ERR_CUDA.
+ * --------------------------------------------------------------------------------------- */
+typedef enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_dtype;
+
+int mxfp4_quant_rows(const void* x, int x_type, int64_t rows, int64_t K, int64_t row_stride,
+                     uint8_t* codes, uint8_t* scales, moe_stream_t stream);
+int mxfp4_dequant_rows(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* y,
+                       int y_type, moe_stream_t stream);
+
+/* out[m, n] = sum_k A[m, k] B[n, k] over MXFP4 rows A [M, K] and B [N, K] as mxfp4_quant_rows
+ * writes them, products exact, accumulated in fp32, rounded once to out_type (MOE_BF16 or MOE_F32).
+ * A row whose scales hold a NaN gives NaN outputs.
+ *   a [M, K/2], b [N, K/2]    16-byte aligned     a_scales [M, K/32], b_scales [N, K/32]  4-byte aligned
+ *   out [M, N]                16-byte aligned
+ * K a multiple of 32, at most 65536; M and N at most 2^22, any parity.  M or N of 0 is a no-op. */
+int mxfp4_matmul(const uint8_t* a, const uint8_t* a_scales, const uint8_t* b, const uint8_t* b_scales,
+                 int64_t M, int64_t N, int64_t K, void* out, int out_type, moe_stream_t stream);
+
+/* The layer with MXFP4 routed experts (gate and up separate), rows as mxfp4_quant_rows writes them:
+ *   gate_f4, up_f4  [E, N, H/2]    gate_e8, up_e8  [E, N, H/32] E8M0
+ *   down_f4         [E, H, N/2]    down_e8         [E, H, N/32] E8M0
+ * (all 16-byte aligned); shared experts as in moe_w4a8_layer. */
+typedef struct {
+    int E, H, N;
+    const uint8_t *gate_f4, *up_f4, *down_f4;
+    const uint8_t *gate_e8, *up_e8, *down_e8;
+    int n_shared, shared_N;
+    const uint16_t *sh_gate, *sh_up, *sh_down;
+} moe_mxfp4_layer;
+
+/* ---------------------------------------------------------------------------------------
+ * The whole layer for a few tokens.
+ *
+ * The layer of moe_w4a8_forward (routing, FP8 of the tokens, gate/up, SwiGLU, FP8 of h, down,
+ * shared experts, combine) for T <= 16 tokens, made for decoding, where the time is the reading of
+ * the touched experts' weights and every launch counts.  W4A8 experts, or MXFP4 experts with
+ *   G[n] = s_x[t] * sum_b 2^(b8_gate[e,n,b] - 127) * sum_{k in b} Xq[t,k] * C_gate[e,n,k]   (likewise U)
+ * and Y from Hq in the same way.  Sums are fp32 in an order of the kernel's own (the same on every
+ * call), so outputs agree with moe_w4a8_forward to rounding, not bit for bit.  The _router forms
+ * compute the logits from the router weight (moe_router_logits' definition).
+ *
+ *   x_bf16 [T, H]   router_logits [T, E] fp32 or wr_bf16 [E, H]   out_bf16 [T, H] (may be x_bf16)
+ *   ws, ws_bytes    device scratch, >= the _workspace_bytes of the layer, T and k; 256-byte
+ *                   aligned, contents on entry ignored; calls that may overlap need their own
+ * Shapes as moe_w4a8_forward with T <= 16, shared_N <= 8192 and H * ceil(T / 8) <= 16384.  Weight
+ * and scale pointers are 16-byte aligned.  T == 0 is a no-op.  The _workspace_bytes calls return 0
+ * for what the layer call refuses.
+ * --------------------------------------------------------------------------------------- */
+size_t moe_w4a8_decode_workspace_bytes(const moe_w4a8_layer* layer, int64_t T, int k);
+int moe_w4a8_decode(const moe_w4a8_layer* layer, const uint16_t* x_bf16, const float* router_logits,
+                    int64_t T, int k, uint16_t* out_bf16, void* ws, size_t ws_bytes,
+                    moe_stream_t stream);
+int moe_w4a8_decode_router(const moe_w4a8_layer* layer, const uint16_t* x_bf16,
+                           const uint16_t* wr_bf16, int64_t T, int k, uint16_t* out_bf16, void* ws,
+                           size_t ws_bytes, moe_stream_t stream);
+size_t moe_mxfp4_decode_workspace_bytes(const moe_mxfp4_layer* layer, int64_t T, int k);
+int moe_mxfp4_decode(const moe_mxfp4_layer* layer, const uint16_t* x_bf16,
+                     const float* router_logits, int64_t T, int k, uint16_t* out_bf16, void* ws,
+                     size_t ws_bytes, moe_stream_t stream);
+int moe_mxfp4_decode_router(const moe_mxfp4_layer* layer, const uint16_t* x_bf16,
+                            const uint16_t* wr_bf16, int64_t T, int k, uint16_t* out_bf16, void* ws,
+                            size_t ws_bytes, moe_stream_t stream);
+
 /* Static description of a status code. */
 const char* moe_status_string(int status);
 

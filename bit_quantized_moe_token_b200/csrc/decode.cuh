@@ -27,30 +27,35 @@
 // loaded by one TMA box for each of its row sets, in the 128-byte swizzle, so a warp reads 16 bytes
 // of eight rows without bank conflicts.
 //
-// The products run on mma.sync m16n8k32 (E4M3): the rows are the M = 16, up to eight tokens the
-// N = 8.  tcgen05 would put 128 rows a tile and the widened weights through TMEM for the same
-// eight columns; here its rate is not needed (16 x 256 weights cost a warp about 150 instructions,
-// a third of the issue slots at the full HBM rate), and a warp's registers hold the whole tile.
-//   INT4:  the stored nibble n = code + 8 is the E4M3 encoding of n 2^-9 (the header of
-//          tc_tiles.cuh); a second MMA with the constant -8 2^-9 takes the offset off, so the
-//          fp32 accumulator holds 2^-9 sum q code exactly as signed codes would.
-//   MXFP4: the nibble s e e m, shifted to s 00ee m00, is the E4M3 encoding of its value 2^-6.
+// The products run on mma.sync m16n8k16 (f16, fp32 sums): the rows are the M = 16, up to eight
+// tokens the N = 8.  tcgen05 would put 128 rows a tile and the widened weights through TMEM for the
+// same eight columns; here its rate is not needed (the stream leaves an SM 1,400 cycles a stage),
+// and a warp's registers hold the whole tile.  E4M3 values are exact in f16, and so are the weights:
+//   INT4:  a nibble n = code + 8 left where it lies in a 16-bit half is the f16 subnormal n 2^-24
+//          (bits 0..3) or n 2^-20 (bits 4..7, whose tokens' values carry 2^-4), so widening a packed
+//          word costs four ANDs and a shift; the accumulator starts at -8 2^-24 sum q, which takes
+//          the offset off again.
+//   MXFP4: cvt.rn.f16x2.e2m1x2.
+// (mma.sync on E4M3 is no way round the conversion: it took 400 warp instructions a stage and warp
+// against 190, and the layer at T = 8 took 213 us.)
 // A group's (block's) partial sum is scaled in fp32 by its weight scale: one promotion every 128
 // (32) weights.  Shared experts run on the bf16 MMA, their activation as bf16 hi + lo halves.
 #pragma once
 #include <cooperative_groups.h>
+#include <type_traits>
 #include "forward.cuh"
 #include "mxfp4.cuh"
 
 namespace moe {
 
 constexpr int kDecodeMaxT = 16;
-constexpr int kDecodeWarps = 16;                         // consumer warps; one more streams the weights
+constexpr int kDecodeWarps = 8;                          // consumer warps; one more streams the weights
 constexpr int kDecodeThreads = 32 * (kDecodeWarps + 1);
 constexpr int kDecodeStage = 32 * 1024;                  // weight bytes of a stage
 constexpr int kDecodeMaxPairs = kDecodeMaxT * kMaxK;
 constexpr int kDecodeMaxSlots = 8;
 constexpr int kDecodeMaxGrid = 256;                      // CTAs the workspace's partial sums provide for
+constexpr int kDecodeBatch = 4;                          // phase A: most stages between two sums over the warps
 constexpr int kDecodePiece = 2048;                       // B-fragment bytes of 256 columns of eight tokens
 
 struct DecodeLayer {
@@ -61,10 +66,11 @@ struct DecodeLayer {
     const uint16_t *sw[3];        // shared experts' gate, up, down (bf16)
 };
 
-// How rows of one weight matrix fill stages: `pieces` of 128 bytes a row; a unit takes 1 << log of
-// a stage's 16 pieces in each of `chunks` stages, 16 >> log units share a stage.
+// How rows of one weight matrix fill stages: `pieces` of 128 bytes a row.  A unit takes 1 << log of a
+// stage's 16 pieces in each of `chunks` stages, and 1 << wlog of the 8 consumer warps, two pieces a
+// warp (one where a row has no more); 8 >> wlog units share a stage.
 struct DecodeRows {
-    int pieces, log, chunks;
+    int pieces, log, wlog, chunks;
 };
 
 struct alignas(64) DecodeParams {
@@ -73,20 +79,20 @@ struct alignas(64) DecodeParams {
     const uint16_t *x, *wr;
     const float* logits;
     uint16_t* out;
-    float *h, *gs, *part, *ws_logits;
+    float *h, *gs, *hsum, *part, *ws_logits;
     uint8_t* hq;
     uint16_t *act_hi, *act_lo;
     unsigned* count;
     DecodeRows ra, rs, rb;        // gate/up, shared gate/up, down (routed; its log serves the shared rows too)
     int shared_chunks;            // stages' worth of a shared down row
     int E, H, N, k, T, n_shared, Ns;
-    int slots, slot_bytes, red_bufs, flat;   // flat: bit i set, map i is 2-D (rows are not whole pieces)
+    int slots, slot_bytes, batch, flat;   // flat: bit i set, map i is 2-D (rows are not whole pieces)
 };
 
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -120,11 +126,10 @@ __device__ __forceinline__ float2 e8m0x2_to_f32(uint32_t b) {
     return make_float2(bf16_bits_to_f32(r.x), bf16_bits_to_f32(r.y));
 }
 
-// Where a lane's eight FP8 codes of columns 8 c8 .. 8 c8 + 7 of token column `col` (0..7) lie in a
-// row of B fragments: pieces of 256 columns; a lane (col, t) reads its 64 bytes of a piece as four
-// 16-byte words i = 2 half + j / 2, each the codes of MMAs j and j + 1 of that half.  MMA j of half
-// h covers columns 32 t + 8 j (INT4: a lane's 16 bytes of a weight row) or 32 j + 8 t (MXFP4: one
-// block an MMA) of the half, t = 0..3.  Returns {piece, byte in the 64-byte rows of a token}.
+// Where the FP8 codes of columns 8 c8 .. 8 c8 + 7 lie in a token's row of B fragments: pieces of
+// 256 columns; lane (token, t) reads its 64 bytes of a piece as four 16-byte words i = 2 h + j / 2, each
+// the codes of weight words j and j + 1 of half h.  Word j of lane t covers columns 32 t + 8 j (INT4:
+// a lane's 16 bytes of a weight row) or 32 j + 8 t (MXFP4: one block a word of the lanes) of the half.
 template <bool kMx>
 __device__ __forceinline__ void frag_place(int c8, int& piece, int& i, int& t, int& odd) {
     const int idx = c8 & 15, h = (c8 >> 4) & 1;
@@ -134,92 +139,141 @@ __device__ __forceinline__ void frag_place(int c8, int& piece, int& i, int& t, i
     i = 2 * h + (j >> 1);
     odd = j & 1;
 }
-
-// acc += the products of one piece (16 rows x 256 weights at row_a / row_b, rows g and g + 8 of the
-// lane's group g) with the B fragments of NT blocks of eight tokens.  sa / sb: the rows' scales at
-// this piece; halves: 128-weight halves of the piece inside the row; live: bit n set, block n has a
-// routed token.
-template <bool kMx, int NT>
-__device__ __forceinline__ void piece_mma(uint32_t row_a, uint32_t row_b, uint32_t sa, uint32_t sb, int halves,
-                                          const uint4 (&b)[NT][4], uint32_t live, float (&acc)[NT][4]) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (h >= halves) break;
-        if constexpr (!kMx) {
-            const uint32_t at = ((h * 4 + t) ^ g) << 4;
-            const uint4 wa = lds128(row_a + at), wb = lds128(row_b + at);
-            const float s0 = lds_bf16(sa + 2 * h), s1 = lds_bf16(sb + 2 * h);
-            float p[NT][4] = {};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t a = word(wa, j), c = word(wb, j);
-                const uint32_t a0 = a & 0x0F0F0F0Fu, a2 = (a >> 4) & 0x0F0F0F0Fu;
-                const uint32_t a1 = c & 0x0F0F0F0Fu, a3 = (c >> 4) & 0x0F0F0F0Fu;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (NT > 1 && !((live >> n) & 1)) continue;
-                    const uint4& q = b[n][2 * h + (j >> 1)];
-                    const uint32_t b0 = j & 1 ? q.z : q.x, b1 = j & 1 ? q.w : q.y;
-                    mma_e4m3(p[n], a0, a1, a2, a3, b0, b1);
-                    mma_e4m3(p[n], 0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u, b0, b1);   // -8 2^-9
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                acc[n][0] = fmaf(s0, p[n][0], acc[n][0]);
-                acc[n][1] = fmaf(s0, p[n][1], acc[n][1]);
-                acc[n][2] = fmaf(s1, p[n][2], acc[n][2]);
-                acc[n][3] = fmaf(s1, p[n][3], acc[n][3]);
-            }
-        } else {
-            const uint32_t ea = lds32(sa + 4 * h), eb = lds32(sb + 4 * h);
-#pragma unroll
-            for (int j2 = 0; j2 < 2; ++j2) {
-                const float2 s0 = e8m0x2_to_f32(ea >> (16 * j2)), s1 = e8m0x2_to_f32(eb >> (16 * j2));
-#pragma unroll
-                for (int jj = 0; jj < 2; ++jj) {
-                    const int j = 2 * j2 + jj;
-                    const uint32_t at = (((h * 4 + j) ^ g) << 4) + 4 * t;
-                    const uint32_t a = lds32(row_a + at), c = lds32(row_b + at);
-                    const uint32_t a0 = ((a << 4) & 0x80808080u) | ((a << 2) & 0x1C1C1C1Cu);
-                    const uint32_t a2 = (a & 0x80808080u) | ((a >> 2) & 0x1C1C1C1Cu);
-                    const uint32_t a1 = ((c << 4) & 0x80808080u) | ((c << 2) & 0x1C1C1C1Cu);
-                    const uint32_t a3 = (c & 0x80808080u) | ((c >> 2) & 0x1C1C1C1Cu);
-                    const float f0 = jj ? s0.y : s0.x, f1 = jj ? s1.y : s1.x;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if (NT > 1 && !((live >> n) & 1)) continue;
-                        const uint4& q = b[n][2 * h + (j >> 1)];
-                        float p[4] = {};
-                        mma_e4m3(p, a0, a1, a2, a3, jj ? q.z : q.x, jj ? q.w : q.y);
-                        acc[n][0] = fmaf(f0, p[0], acc[n][0]);
-                        acc[n][1] = fmaf(f0, p[1], acc[n][1]);
-                        acc[n][2] = fmaf(f1, p[2], acc[n][2]);
-                        acc[n][3] = fmaf(f1, p[3], acc[n][3]);
-                    }
-                }
-            }
-        }
+// Eight codes in column order -> the order in which the weights' widening pairs them: for INT4 the
+// nibbles of a word come out as (0,4) (1,5) (2,6) (3,7), for MXFP4 as they are.
+template <bool kMx>
+__device__ __forceinline__ uint2 frag_order(uint2 c) {
+    return kMx ? c : make_uint2(__byte_perm(c.x, c.y, 0x5140), __byte_perm(c.x, c.y, 0x7362));
+}
+// Four codes in that order -> the two B registers of one MMA.
+template <bool kMx>
+__device__ __forceinline__ void frag_f16(uint32_t c, uint32_t& b0, uint32_t& b1) {
+    const __half2_raw l = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c & 0xFFFFu), __NV_E4M3);
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c >> 16), __NV_E4M3);
+    b0 = *reinterpret_cast<const uint32_t*>(&l);
+    b1 = *reinterpret_cast<const uint32_t*>(&h);
+    if constexpr (!kMx) {   // the nibbles in bits 4..7 stand for 16 n
+        const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h), __half2half2(__ushort_as_half(0x2C00)));   // 2^-4
+        b1 = *reinterpret_cast<const uint32_t*>(&v);
     }
 }
-// The power of two that piece_mma's sums lack (the E4M3 encodings of the weights).
-template <bool kMx>
-constexpr float kDecodeLadder = kMx ? 64.0f : 512.0f;
+constexpr float kNibbleOffset = -8.0f / 16777216.0f;   // -8 2^-24
 
-// The same for 16 rows x 64 bf16 weights; b: the lane's eight values of each half (32 columns).
-template <int NT>
-__device__ __forceinline__ void piece_mma_bf16(uint32_t row_a, uint32_t row_b, const uint4 (&b)[NT][2], float (&acc)[NT][4]) {
+// A warp's B fragments of one block of eight tokens: the 512 columns of its two pieces as f16 (four
+// halves of 128 columns), from the FP8 codes.
+template <bool kMx>
+__device__ __forceinline__ void frags_f16(const uint4 (&q)[8], uint32_t (&f)[64]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) frag_f16<kMx>(word(q[i >> 2], i & 3), f[2 * i], f[2 * i + 1]);
+}
+// INT4: where the accumulators start, off[h] = -8 2^-24 sum_q over half h, for the lane's two
+// token columns.
+__device__ __forceinline__ void nibble_offsets(const uint32_t (&f)[64], float2 (&off)[4]) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        float p[4] = {};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)   // -8 2^-24, -8 2^-20
+            mma_f16(p, 0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u, f[16 * h + 2 * i], f[16 * h + 2 * i + 1]);
+        off[h] = make_float2(p[0], p[1]);
+    }
+}
+
+// Two E2M1 codes (the low byte of c) -> f16x2, the low nibble first.
+__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t c) {
+    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(c & 0xFFu), __NV_E2M1);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// acc += the products of 16 rows x 512 weights (two pieces, `step` bytes apart in the stage) with the
+// B fragments of one block of tokens.  row_a / row_b: the lane's rows g and g + 8; sa / sb: those
+// rows' scales at the first piece; halves: how many of the four 128-column halves lie inside the row
+// (a missing one has fragments and offsets of zero, and its scale is taken as nothing).  Nothing
+// branches, so the halves' loads and MMA chains overlap.
+template <bool kMx>
+__device__ __forceinline__ void pieces_mma(uint32_t row_a, uint32_t row_b, uint32_t step, uint32_t sa, uint32_t sb,
+                                           int halves, const uint32_t (&f)[64], const float2 (&off)[4], float (&acc)[4]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    if constexpr (!kMx) {
+        const uint32_t at0 = (t ^ g) << 4;
+        float s0[4], s1[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            s0[h] = h < halves ? lds_bf16(sa + 2 * h) : 0.0f;
+            s1[h] = h < halves ? lds_bf16(sb + 2 * h) : 0.0f;
+        }
+#pragma unroll
+        for (int pc = 0; pc < 2; ++pc) {
+            uint4 wa[2], wb[2];
+            float p[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                wa[h] = lds128(row_a + pc * step + (at0 ^ (h * 64)));
+                wb[h] = lds128(row_b + pc * step + (at0 ^ (h * 64)));
+                p[h][0] = p[h][2] = off[2 * pc + h].x;
+                p[h][1] = p[h][3] = off[2 * pc + h].y;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t a = word(wa[h], j) >> (8 * s), c = word(wb[h], j) >> (8 * s);
+                        const int i = 16 * (2 * pc + h) + 4 * j + 2 * s;
+                        mma_f16(p[h], a & 0x000F000Fu, c & 0x000F000Fu, a & 0x00F000F0u, c & 0x00F000F0u, f[i], f[i + 1]);
+                    }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                acc[0] = fmaf(s0[2 * pc + h], p[h][0], acc[0]);
+                acc[1] = fmaf(s0[2 * pc + h], p[h][1], acc[1]);
+                acc[2] = fmaf(s1[2 * pc + h], p[h][2], acc[2]);
+                acc[3] = fmaf(s1[2 * pc + h], p[h][3], acc[3]);
+            }
+        }
+    } else {
+        uint32_t ea[4], eb[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            ea[h] = h < halves ? lds32(sa + 4 * h) : 0u;
+            eb[h] = h < halves ? lds32(sb + 4 * h) : 0u;
+        }
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t at = (h >> 1) * step + ((((h & 1) * 4 + j) ^ g) << 4) + 4 * t;
+                const uint32_t a = lds32(row_a + at), c = lds32(row_b + at);
+                const float2 e0 = e8m0x2_to_f32(ea[h] >> (16 * (j >> 1))), e1 = e8m0x2_to_f32(eb[h] >> (16 * (j >> 1)));
+                const float f0 = j & 1 ? e0.y : e0.x, f1 = j & 1 ? e1.y : e1.x;
+                float p[4] = {};
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const int i = 16 * h + 4 * j + 2 * s;
+                    mma_f16(p, e2m1x2_to_f16x2(a >> (16 * s)), e2m1x2_to_f16x2(c >> (16 * s)),
+                            e2m1x2_to_f16x2(a >> (16 * s + 8)), e2m1x2_to_f16x2(c >> (16 * s + 8)), f[i], f[i + 1]);
+                }
+                acc[0] = fmaf(f0, p[0], acc[0]);
+                acc[1] = fmaf(f0, p[1], acc[1]);
+                acc[2] = fmaf(f1, p[2], acc[2]);
+                acc[3] = fmaf(f1, p[3], acc[3]);
+            }
+    }
+}
+// The power of two that pieces_mma's sums lack.
+template <bool kMx>
+constexpr float kDecodeLadder = kMx ? 1.0f : 16777216.0f;
+
+// The same for 16 rows x 64 bf16 weights of one piece and one block of tokens; b: the lane's eight
+// values of each half (32 columns).
+__device__ __forceinline__ void piece_mma_bf16(uint32_t row_a, uint32_t row_b, const uint4 (&b)[2], float (&acc)[4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const uint32_t at = ((h * 4 + t) ^ g) << 4;
         const uint4 wa = lds128(row_a + at), wb = lds128(row_b + at);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            mma_bf16(acc[n], wa.x, wb.x, wa.y, wb.y, b[n][h].x, b[n][h].y);
-            mma_bf16(acc[n], wa.z, wb.z, wa.w, wb.w, b[n][h].z, b[n][h].w);
-        }
+        mma_bf16(acc, wa.x, wb.x, wa.y, wb.y, b[h].x, b[h].y);
+        mma_bf16(acc, wa.z, wb.z, wa.w, wb.w, b[h].z, b[h].w);
     }
 }
 
@@ -246,6 +300,41 @@ __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;
 
 // The first unit of CTA c's even share of n units.
 __device__ __forceinline__ int share(int n, int c, int G) { return static_cast<int>((int64_t)n * c / G); }
+
+// S2 of one token by one warp, as topk_row (ranked by logit descending, index ascending; NaN as
+// -inf), with the warp's maximum and the lowest index that has it in two redux instructions: the
+// stream waits for this.  A logit's key is its bits in the order of the values, 0 once taken.
+template <int EPL>
+__device__ __forceinline__ void rank_row(const float* l, int E, int k, int* ids, float* gates, int lane) {
+    uint32_t key[EPL];
+#pragma unroll
+    for (int s = 0; s < EPL; ++s) {
+        const int e = lane + 32 * s;
+        float x = e < E ? __ldcg(l + e) : 0.0f;
+        x = isnan(x) ? -INFINITY : x + 0.0f;   // -0 ties with +0
+        const uint32_t u = __float_as_uint(x);
+        key[s] = e < E ? (u & 0x80000000u ? ~u : u | 0x80000000u) : 0u;
+    }
+    float first = 0.0f, sum = 0.0f, mine = 0.0f;
+    for (int j = 0; j < k; ++j) {
+        uint32_t best = 0u;
+#pragma unroll
+        for (int s = 0; s < EPL; ++s) best = max(best, key[s]);
+        best = __reduce_max_sync(0xffffffffu, best);
+        int at = 0x7FFFFFFF;
+#pragma unroll
+        for (int s = EPL - 1; s >= 0; --s) at = key[s] == best ? lane + 32 * s : at;
+        at = __reduce_min_sync(0xffffffffu, at);
+#pragma unroll
+        for (int s = 0; s < EPL; ++s) key[s] = at == lane + 32 * s ? 0u : key[s];
+        const float v = __uint_as_float(best & 0x80000000u ? best & 0x7FFFFFFFu : ~best);
+        if (j == 0) first = v;
+        const float e = expf(v - first);
+        sum = __fadd_rn(sum, e);
+        if (lane == j) { ids[j] = at; mine = e; }
+    }
+    if (lane < k) gates[lane] = __fdiv_rn(mine, sum);
+}
 
 // A wait ran out: the status word is set, and the warp stays until its CTA's copies in flight (microseconds) have landed.
 __device__ __forceinline__ void give_up() {
@@ -308,21 +397,23 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
     for (int i = cta * kDecodeThreads + threadIdx.x; i < tiles; i += G * kDecodeThreads) p.count[i] = 0u;
     __syncthreads();
 
-    // max |x| of the tokens: 16 / (T rounded up to a power of two) warps a token
-    const int twarps = kDecodeWarps >> (T > 8 ? 4 : T > 4 ? 3 : T > 2 ? 2 : T > 1 ? 1 : 0);
-    const int tok = warp / twarps, tpart = warp % twarps;
-    const uint4* xrow = reinterpret_cast<const uint4*>(p.x + (int64_t)tok * p.H);
-    if (!producer && tok < T) {
-        float a = 0.0f;
-        for (int c = tpart * 32 + lane; c < p.H / 8; c += twarps * 32) a = fmaxf(a, amax8(__ldg(xrow + c)));
-        a = warp_max(a);
-        if (lane == 0) atomicMax(&S.amax[tok], __float_as_uint(a));
+    // max |x| of the tokens: 8 / (T rounded up to a power of two) warps a token
+    const int twarps = kDecodeWarps >> (T > 4 ? 3 : T > 2 ? 2 : T > 1 ? 1 : 0);
+    const int tok0 = warp / twarps, tpart = warp % twarps;
+    if (!producer) {
+        for (int tok = tok0; tok < T; tok += kDecodeWarps / twarps) {
+            const uint4* xrow = reinterpret_cast<const uint4*>(p.x + (int64_t)tok * p.H);
+            float a = 0.0f;
+            for (int c = tpart * 32 + lane; c < p.H / 8; c += twarps * 32) a = fmaxf(a, amax8(__ldg(xrow + c)));
+            a = warp_max(a);
+            if (lane == 0) atomicMax(&S.amax[tok], __float_as_uint(a));
+        }
     }
 
     const float* logits = p.logits;
-    if (p.wr) {   // logits of experts 2 c and 2 c + 1, then of those 2 G further: eight warps an expert
+    if (p.wr) {   // logits of experts 2 c and 2 c + 1, then of those 2 G further: four warps an expert
         logits = p.ws_logits;
-        const int half = warp >> 3, part = warp & 7, HC = p.H / 8;
+        const int half = warp >> 2, part = warp & 3, HC = p.H / 8;
         for (int e0 = 2 * cta; e0 < p.E; e0 += 2 * G) {
             const int e = e0 + half;
             float acc[8 * NT];
@@ -330,7 +421,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
             for (int j = 0; j < 8 * NT; ++j) acc[j] = 0.0f;
             if (!producer && e < p.E) {
                 const uint4* w4 = reinterpret_cast<const uint4*>(p.wr + (int64_t)e * p.H);
-                for (int c = part * 32 + lane; c < HC; c += 256) {
+                for (int c = part * 32 + lane; c < HC; c += 128) {
                     float wf[8];
                     bf16x8_to_f32(__ldg(w4 + c), wf);
 #pragma unroll
@@ -355,7 +446,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
                 if (e0 + hh < p.E) {
                     float s = 0.0f;
 #pragma unroll
-                    for (int w = 0; w < 8; ++w) s += red[(hh * 8 + w) * 8 * NT + j];
+                    for (int w = 0; w < 4; ++w) s += red[(hh * 4 + w) * 8 * NT + j];
                     p.ws_logits[(int64_t)j * p.E + e0 + hh] = s;
                 }
             }
@@ -364,18 +455,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
         cg::this_grid().sync();
     }
 
-    // S2: token t by warp 16 - t (the streaming warp has nothing else to do yet)
-    {
-        const int tt = kDecodeWarps - warp;
-        if (tt < T) {
-            const float* l = logits + (int64_t)tt * p.E;
-            int* ids = S.ids + tt * k;
-            float* gates = S.gates + tt * k;
-            if (p.E <= 256) topk_row<8, true>(l, p.E, k, ids, gates, lane);
-            else topk_row<32, true>(l, p.E, k, ids, gates, lane);
-            __syncwarp();
-            if (lane < k) atomicOr(&S.bitmap[ids[lane] >> 5], 1u << (ids[lane] & 31));
-        }
+    // S2: a warp a token, the streaming warp (which has nothing else to do yet) first
+    for (int tt = kDecodeWarps - warp; tt < T; tt += kDecodeWarps + 1) {
+        const float* l = logits + (int64_t)tt * p.E;
+        int* ids = S.ids + tt * k;
+        float* gates = S.gates + tt * k;
+        if (p.E <= 256) rank_row<8>(l, p.E, k, ids, gates, lane);
+        else rank_row<kMaxE / 32>(l, p.E, k, ids, gates, lane);
+        __syncwarp();
+        if (lane < k) atomicOr(&S.bitmap[ids[lane] >> 5], 1u << (ids[lane] & 31));
     }
     __syncthreads();
     if (threadIdx.x < P) {   // the pair's expert's place among the touched ones
@@ -425,7 +513,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
         for (int pass = 0; pass < 2; ++pass) {   // phase A: routed units, then the shared experts'
             const DecodeRows& R = pass ? p.rs : p.ra;
             const int u0 = pass ? s0 : a0, u1 = pass ? s1 : a1, per = pass ? nbs : nb, rows = pass ? p.Ns : p.N;
-            const int upu = 16 >> R.log;
+            const int upu = kDecodeWarps >> R.wlog;
             for (int u = u0; ok && u < u1; u += upu) {
                 const int n = min(upu, u1 - u);
                 for (int c = 0; ok && c < R.chunks; ++c) {
@@ -448,7 +536,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
         }
         // phase B: as many stages as there are slots before the barriers, the rest after them
         int issued = 0, synced = 0;
-        const int upu = 16 >> p.rb.log;
+        const int upu = kDecodeWarps >> p.rb.wlog;
         for (int v = v0; ok && v < v1;) {
             const int tile = v / V, lo = v - tile * V, hi = min(V, lo + v1 - v);
             for (int q = lo; ok && q < hi; q += upu) {
@@ -487,10 +575,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
 
     // ---- the consumer warps ----
     // S1: the tokens' FP8 codes as B fragments
-    if (tok < T) {
+    for (int tok = tok0; tok < T; tok += kDecodeWarps / twarps) {
+        const uint4* xrow = reinterpret_cast<const uint4*>(p.x + (int64_t)tok * p.H);
         const float s = __fdiv_rn(__uint_as_float(S.amax[tok]), kFp8Max);
         for (int c = tpart * 32 + lane; c < p.H / 8; c += twarps * 32) {
-            const uint2 q = perm8(quant8(__ldg(xrow + c), s));
+            const uint2 q = frag_order<kMx>(quant8(__ldg(xrow + c), s));
             int piece, i, tt, odd;
             frag_place<kMx>(c, piece, i, tt, odd);
             const uint32_t at = frags + ((piece * NT + (tok >> 3)) * 4 + i) * 512 + ((tok & 7) * 4 + tt) * 16 + odd * 8;
@@ -501,112 +590,137 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
 
     DecodeRing r;
     bool ok = true;
-    int buf = 0;
-    const int red_words = kDecodeWarps * NT * 128;
     auto wait_full = [&]() { ok = ok && ws::wait(&S.full[r.slot], r.phase, &S.abort); };
     auto release = [&]() {
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&S.empty[r.slot]);
         r.next(p.slots);
     };
-    // Leaves every warp's sums in `red` and returns the buffer; the caller reads it before the next call.
-    auto share_sums = [&](const float (&acc)[NT][4]) {
-        float* dst = red + buf * red_words;
-        if (p.red_bufs > 1) buf ^= 1;
-        else consumers_sync();                        // the last readers of the one buffer are done
+    // This warp's sums into set `s` of `red` (one float a lane and register: no bank conflicts).
+    auto put_sums = [&](int s, const float (&acc)[NT][4]) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dst[(warp * NT * 4 + n * 4 + i) * 32 + lane] = acc[n][i];
-        consumers_sync();
-        return dst;
+            for (int i = 0; i < 4; ++i) red[((s * kDecodeWarps + warp) * NT * 4 + n * 4 + i) * 32 + lane] = acc[n][i];
     };
+    // The gate and up sums of output s (unit, token column, row g) of a set of stages.
+    auto get_sums = [&](int s, int wlog, int& unit, int& col, float& gate, float& up) {
+        const int c1 = (s >> 5) & 1, n = (s >> 6) % NT, per = 1 << wlog;
+        unit = s / (64 * NT);
+        col = n * 8 + t * 2 + c1;
+        gate = up = 0.0f;
+        const float* f = red + ((unit << wlog) * NT * 4 + n * 4 + c1) * 32 + lane;
+        for (int w = 0; w < per; ++w) {
+            gate += f[w * NT * 128];
+            up += f[w * NT * 128 + 64];
+        }
+    };
+    const int batch = p.batch;
 
-    // phase A, routed units: h = silu(G) U
-    for (int u = a0; u < a1; u += 16 >> p.ra.log) {
-        const int slot_unit = warp >> p.ra.log, piece0 = warp & ((1 << p.ra.log) - 1);
-        const int uu = u + slot_unit, ei = uu / nb;
-        float acc[NT][4] = {};
-        uint32_t live = 0;
-        if (uu < a1) {
-            const uint32_t toks = S.tokens[ei];
+    // phase A, routed units: h = silu(G) U.  A batch of stages, then their sums over the warps.
+    {
+        const int upu = kDecodeWarps >> p.ra.wlog, slot_unit = warp >> p.ra.wlog;
+        const int pair0 = warp & ((1 << p.ra.wlog) - 1);          // which two pieces of a chunk
+        const uint32_t row_off = slot_unit * (2048 << p.ra.log) + 2 * pair0 * 1024 + g * 128, row_b = 1024 << p.ra.log;
+        const uint32_t sc_off = kDecodeStage + (slot_unit * 16 + g) * row_scale_a;
+        uint32_t f[64];
+        float2 off[4];
+        int held = -1;   // what f holds: two pieces of one block of tokens
+        int ei = a0 / nb, left = nb - a0 % nb;   // the expert of unit u and how many of its units are left
+        for (int u = a0; u < a1; u += upu * batch) {
+#pragma unroll 1
+            for (int s = 0; s < batch && u + s * upu < a1; ++s) {
+                int e = ei;                      // this warp's expert
+                for (int ahead = s * upu + slot_unit - left; ahead >= 0; ahead -= nb) ++e;
+                const bool mine = u + s * upu + slot_unit < a1;
+                const uint32_t toks = NT > 1 && mine ? S.tokens[e] : 0xFFu;
+                float acc[NT][4] = {};
+                for (int c = 0; c < p.ra.chunks; ++c) {
+                    const int pair = c * 8 + pair0, halves = p.H / 128 - 4 * pair;
+                    wait_full();
+                    if (ok && mine && halves > 0) {
+                        const uint32_t base = ring + r.slot * p.slot_bytes;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) live |= (toks >> (8 * n) & 0xFFu) ? 1u << n : 0u;
-        }
-        for (int c = 0; c < p.ra.chunks; ++c) {
-            wait_full();
-            const int piece = c * 16 + piece0, halves = min(2, p.H / 128 - 2 * piece);
-            if (ok && uu < a1 && halves > 0) {
-                const uint32_t base = ring + r.slot * p.slot_bytes;
-                const uint32_t row = base + slot_unit * (2048 << p.ra.log) + piece0 * 1024 + g * 128;
-                const uint32_t sc = base + kDecodeStage + (slot_unit * 16 + g) * row_scale_a + piece * (kMx ? 8 : 4);
-                uint4 b[NT][4];
+                        for (int n = 0; n < NT; ++n) {
+                            if (NT > 1 && !((toks >> (8 * n)) & 0xFFu)) continue;
+                            if (held != pair * NT + n) {
+                                held = pair * NT + n;
+                                uint4 q[8];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) b[n][i] = lds128(frags + ((piece * NT + n) * 4 + i) * 512 + lane * 16);
-                piece_mma<kMx, NT>(row, row + (1024 << p.ra.log), sc, sc + 8 * row_scale_a, halves, b, live, acc);
+                                for (int i = 0; i < 8; ++i)
+                                    q[i] = i < 2 * halves ? lds128(frags + (((2 * pair + (i >> 2)) * NT + n) * 4 + (i & 3)) * 512 + lane * 16)
+                                                          : make_uint4(0u, 0u, 0u, 0u);
+                                frags_f16<kMx>(q, f);
+                                if constexpr (!kMx) nibble_offsets(f, off);
+                            }
+                            pieces_mma<kMx>(base + row_off, base + row_off + row_b, 1024, base + sc_off + pair * (kMx ? 16 : 8),
+                                            base + sc_off + 8 * row_scale_a + pair * (kMx ? 16 : 8), halves, f, off, acc[n]);
+                        }
+                    }
+                    release();
+                }
+                put_sums(s, acc);
             }
-            release();
-        }
-        const float* sums = share_sums(acc);
-        const int per = 1 << p.ra.log, n_out = (16 >> p.ra.log) * 64 * NT;
-        for (int s = threadIdx.x; s < n_out; s += 32 * kDecodeWarps) {
-            const int c1 = (s >> 5) & 1, n = (s >> 6) % NT, q = s / (64 * NT);
-            const int col = n * 8 + t * 2 + c1, unit = u + q;
-            if (col >= T || unit >= a1) continue;
-            const int e = unit / nb;
-            if (!((S.tokens[e] >> col) & 1u)) continue;
-            float gt = 0.0f, up = 0.0f;
-            for (int w = 0; w < per; ++w) {
-                const float* f = sums + ((q * per + w) * NT * 4 + n * 4 + c1) * 32 + lane;
-                gt += f[0];
-                up += f[64];
+            consumers_sync();
+            const int n_out = min(batch * upu, a1 - u) * 64 * NT;
+            for (int s = threadIdx.x; s < n_out; s += 32 * kDecodeWarps) {
+                int unit, col;
+                float gt, up;
+                get_sums(s, p.ra.wlog, unit, col, gt, up);
+                int e = ei, b = unit + nb - left;
+                for (; b >= nb; b -= nb) ++e;
+                if (col >= T || !((S.tokens[e] >> col) & 1u)) continue;
+                const float sx = __fdiv_rn(__uint_as_float(S.amax[col]), kFp8Max) * kDecodeLadder<kMx>;
+                p.h[(int64_t)(col * k + S.pick[e][col]) * p.N + b * 8 + g] = silu(gt * sx) * (up * sx);
             }
-            const float sx = __fdiv_rn(__uint_as_float(S.amax[col]), kFp8Max) * kDecodeLadder<kMx>;
-            p.h[(int64_t)(col * k + S.pick[e][col]) * p.N + (unit % nb) * 8 + g] = silu(gt * sx) * (up * sx);
+            consumers_sync();
+            for (left -= upu * batch; left <= 0; left += nb) ++ei;
         }
     }
     // phase A, shared experts: the same on bf16 weights and tokens
-    for (int u = s0; u < s1; u += 16 >> p.rs.log) {
-        const int slot_unit = warp >> p.rs.log, piece0 = warp & ((1 << p.rs.log) - 1);
-        float acc[NT][4] = {};
-        for (int c = 0; c < p.rs.chunks; ++c) {
-            const int piece = c * 16 + piece0;
-            const bool mine = u + slot_unit < s1 && piece < p.rs.pieces;
-            uint4 b[NT][2] = {};
-            if (mine) {
+    {
+        const int upu = kDecodeWarps >> p.rs.wlog, slot_unit = warp >> p.rs.wlog;
+        const int pair0 = warp & ((1 << p.rs.wlog) - 1);
+        const uint32_t row_off = slot_unit * (2048 << p.rs.log) + 2 * pair0 * 1024 + g * 128, row_b = 1024 << p.rs.log;
+        for (int u = s0; u < s1; u += upu) {
+            float acc[NT][4] = {};
+            for (int c = 0; c < p.rs.chunks; ++c) {
+                const int piece = 2 * (c * 8 + pair0);
+                const bool mine = u + slot_unit < s1 && piece < p.rs.pieces;   // pieces: even, 2 H bytes
+                uint4 b[NT][2][2] = {};
+                if (mine) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (n * 8 + g < T)
-                            b[n][h] = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)(n * 8 + g) * p.H) + piece * 8 + h * 4 + t);
+                        for (int i = 0; i < 4; ++i)
+                            if (n * 8 + g < T)
+                                b[n][i >> 1][i & 1] = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)(n * 8 + g) * p.H) + piece * 8 + i * 4 + t);
+                }
+                wait_full();
+                if (ok && mine) {
+                    const uint32_t row = ring + r.slot * p.slot_bytes + row_off;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int pc = 0; pc < 2; ++pc) piece_mma_bf16(row + pc * 1024, row + row_b + pc * 1024, b[n][pc], acc[n]);
+                }
+                release();
             }
-            wait_full();
-            if (ok && mine) {
-                const uint32_t row = ring + r.slot * p.slot_bytes + slot_unit * (2048 << p.rs.log) + piece0 * 1024 + g * 128;
-                piece_mma_bf16<NT>(row, row + (1024 << p.rs.log), b, acc);
+            put_sums(0, acc);
+            consumers_sync();
+            const int n_out = min(upu, s1 - u) * 64 * NT;
+            for (int s = threadIdx.x; s < n_out; s += 32 * kDecodeWarps) {
+                int unit, col;
+                float gt, up;
+                get_sums(s, p.rs.wlog, unit, col, gt, up);
+                if (col >= T) continue;
+                const float a = silu(gt) * up;
+                const uint16_t hi = f32_to_bf16_bits(a);   // hi + lo: 16 bits of the activation
+                const int64_t at = (int64_t)col * p.n_shared * p.Ns + (u + unit) * 8 + g;
+                p.act_hi[at] = hi;
+                p.act_lo[at] = f32_to_bf16_bits(a - bf16_bits_to_f32(hi));
             }
-            release();
-        }
-        const float* sums = share_sums(acc);
-        const int per = 1 << p.rs.log, n_out = (16 >> p.rs.log) * 64 * NT;
-        for (int s = threadIdx.x; s < n_out; s += 32 * kDecodeWarps) {
-            const int c1 = (s >> 5) & 1, n = (s >> 6) % NT, q = s / (64 * NT);
-            const int col = n * 8 + t * 2 + c1, unit = u + q;
-            if (col >= T || unit >= s1) continue;
-            float gt = 0.0f, up = 0.0f;
-            for (int w = 0; w < per; ++w) {
-                const float* f = sums + ((q * per + w) * NT * 4 + n * 4 + c1) * 32 + lane;
-                gt += f[0];
-                up += f[64];
-            }
-            const float a = silu(gt) * up;
-            const uint16_t hi = f32_to_bf16_bits(a);   // hi + lo: 16 bits of the activation
-            const int64_t at = (int64_t)col * p.n_shared * p.Ns + unit * 8 + g;
-            p.act_hi[at] = hi;
-            p.act_lo[at] = f32_to_bf16_bits(a - bf16_bits_to_f32(hi));
+            consumers_sync();
         }
     }
 
@@ -626,7 +740,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
         consumers_sync();
         a = warp_max(S.red[lane & (kDecodeWarps - 1)]);
         const float s = __fdiv_rn(a, kFp8Max);
-        for (int c = threadIdx.x; c < p.N / 8; c += 32 * kDecodeWarps) {
+        for (int c = threadIdx.x; c < p.N / 8; c += 32 * kDecodeWarps) {   // whole half-warps: N is a multiple of 128
             uint2 codes = make_uint2(0u, 0u);
             if (s != 0.0f) {
                 const float4 v = __ldcg(src + 2 * c), w = __ldcg(src + 2 * c + 1);
@@ -637,7 +751,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
             }
             int piece, i, tt, odd;
             frag_place<kMx>(c, piece, i, tt, odd);
-            *reinterpret_cast<uint2*>(p.hq + (int64_t)q * hq_row + piece * 256 + i * 64 + tt * 16 + odd * 8) = perm8(codes);
+            *reinterpret_cast<uint2*>(p.hq + (int64_t)q * hq_row + piece * 256 + i * 64 + tt * 16 + odd * 8) =
+                frag_order<kMx>(codes);
+            if constexpr (!kMx) {   // the sums of the 128-column groups, for the nibbles' offset
+                float sum = e4m3x8_sum(codes);
+                const uint32_t half = 0xFFFFu << (lane & 16);
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(half, sum, o);
+                if ((c & 15) == 0) p.hsum[(int64_t)q * (hq_row / 128) + (c >> 4)] = sum * kNibbleOffset;
+            }
         }
         if (threadIdx.x == 0) p.gs[q] = S.gates[q] * s * kDecodeLadder<kMx>;
     }
@@ -645,82 +767,122 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
     if (threadIdx.x < P) S.gs[threadIdx.x] = __ldcg(p.gs + threadIdx.x);
     consumers_sync();
 
-    // phase B
-    const int upu = 16 >> p.rb.log, slot_unit = warp >> p.rb.log, piece0 = warp & ((1 << p.rb.log) - 1);
+    // phase B.  The FP8 activations of a warp's next stage (its first block of tokens) are fetched
+    // while it works on this one.
+    const int upu = kDecodeWarps >> p.rb.wlog, slot_unit = warp >> p.rb.wlog;
+    const int pair0 = warp & ((1 << p.rb.wlog) - 1), pairs = 1 << p.rb.wlog;   // of a unit
+    const uint32_t row_off = slot_unit * (2048 << p.rb.log) + 2 * pair0 * 2048 + g * 128;
+    const uint32_t sc_off = kDecodeStage + (slot_unit * 16 + g) * row_scale_b;
+    uint4 q[8] = {};
+    float2 off[4] = {};
+    // Block n of routed expert ei's activations at columns 512 pair ..
+    auto fetch = [&](int ei, int pair, int n) {
+        const int halves = p.N / 128 - 4 * pair, col = n * 8 + g;
+        const uint32_t toks = S.tokens[ei];
+        const bool on = (toks >> col) & 1u;
+        const uint4* src = reinterpret_cast<const uint4*>(p.hq + (int64_t)(on ? col * k + S.pick[ei][col] : 0) * hq_row + pair * 512) + t;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = on && i < 2 * halves ? __ldcg(src + (i >> 2) * 16 + (i & 3) * 4) : make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (!kMx) {
+            float f[2][4] = {};
+#pragma unroll
+            for (int c1 = 0; c1 < 2; ++c1) {
+                const int c2 = n * 8 + t * 2 + c1;
+                if ((toks >> c2) & 1u) {
+                    const float* hs = p.hsum + (int64_t)(c2 * k + S.pick[ei][c2]) * (hq_row / 128) + 4 * pair;
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) f[c1][h] = h < halves ? __ldcg(hs + h) : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 4; ++h) off[h] = make_float2(f[0][h], f[1][h]);
+        }
+    };
+    auto first_block = [&](int ei) { return NT > 1 && !(S.tokens[ei] & 0xFFu) ? 1 : 0; };
+    // The next stage's first block, where the warp's unit there is a routed expert's.
+    auto prefetch = [&](int id, int hi) {
+        if (id < hi && id < Vr) fetch(id / p.rb.chunks, (id % p.rb.chunks) * pairs + pair0, first_block(id / p.rb.chunks));
+    };
     for (int v = v0; v < v1;) {
         const int tile = v / V, lo = v - tile * V, hi = min(V, lo + v1 - v);
         float acc[NT][4] = {};
-        for (int q = lo; q < hi; q += upu) {
-            const int id = q + slot_unit;
-            const bool mine = id < hi, routed = id < Vr;
-            const int per = routed ? p.rb.chunks : p.shared_chunks, o = routed ? id : id - Vr;
-            const int ei = o / per, piece = ((o % per) << p.rb.log) + piece0;
+        prefetch(lo + slot_unit, hi);
+        for (int u = lo; u < hi; u += upu) {
+            const int id = u + slot_unit;
             const uint32_t base = ring + r.slot * p.slot_bytes;
-            const uint32_t row = base + slot_unit * (2048 << p.rb.log) + piece0 * 2048 + g * 128;
-            if (mine && routed) {
-                const int halves = min(2, p.N / 128 - 2 * piece);
+            if (id < Vr && id < hi) {
+                const int ei = id / p.rb.chunks, pair = (id % p.rb.chunks) * pairs + pair0, halves = p.N / 128 - 4 * pair;
                 const uint32_t toks = S.tokens[ei];
-                uint4 b[NT][4] = {};
-                uint32_t live = 0;
-                if (halves > 0) {
+                uint32_t f[64];
+                float2 o[4];
+                frags_f16<kMx>(q, f);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        live |= (toks >> (8 * n) & 0xFFu) ? 1u << n : 0u;
-                        const int col = n * 8 + g;
-                        if ((toks >> col) & 1u) {
-                            const uint4* src = reinterpret_cast<const uint4*>(
-                                p.hq + (int64_t)(col * k + S.pick[ei][col]) * hq_row + piece * 256) + t;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) b[n][i] = __ldcg(src + i * 4);
-                        }
-                    }
-                }
+                for (int h = 0; h < 4; ++h) o[h] = off[h];
+                prefetch(id + upu, hi);
                 wait_full();
                 if (ok && halves > 0) {
-                    float y[NT][4] = {};
-                    const uint32_t sc = base + kDecodeStage + (slot_unit * 16 + g) * row_scale_b + piece * (kMx ? 8 : 4);
-                    piece_mma<kMx, NT>(row, row + 1024, sc, sc + 8 * row_scale_b, halves, b, live, y);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < NT; ++n) {
+                        if (NT > 1 && !((toks >> (8 * n)) & 0xFFu)) continue;
+                        if (NT > 1 && n != first_block(ei)) {      // a second block: fetched now, the next stage's again after it
+                            fetch(ei, pair, n);
+                            frags_f16<kMx>(q, f);
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) o[h] = off[h];
+                            prefetch(id + upu, hi);
+                        }
+                        float y[4] = {};
+                        pieces_mma<kMx>(base + row_off, base + row_off + 1024, 2048, base + sc_off + pair * (kMx ? 16 : 8),
+                                        base + sc_off + 8 * row_scale_b + pair * (kMx ? 16 : 8), halves, f, o, y);
 #pragma unroll
                         for (int c1 = 0; c1 < 2; ++c1) {
                             const int col = n * 8 + t * 2 + c1;
                             if ((toks >> col) & 1u) {   // the other columns hold nothing of this expert's
-                                const float f = S.gs[col * k + S.pick[ei][col]];
-                                acc[n][c1] = fmaf(f, y[n][c1], acc[n][c1]);
-                                acc[n][c1 + 2] = fmaf(f, y[n][c1 + 2], acc[n][c1 + 2]);
+                                const float fac = S.gs[col * k + S.pick[ei][col]];
+                                acc[n][c1] = fmaf(fac, y[c1], acc[n][c1]);
+                                acc[n][c1 + 2] = fmaf(fac, y[c1 + 2], acc[n][c1 + 2]);
                             }
                         }
+                    }
                 }
             } else {
-                uint4 bh[NT][2] = {}, bl[NT][2] = {};
-                const bool live = mine && piece < p.Ns / 64;
-                if (live) {
+                const int o = id - Vr, e = o / max(1, p.shared_chunks), piece = ((o % max(1, p.shared_chunks)) << p.rb.log) + 2 * pair0;
+                const bool mine = id < hi && piece < p.Ns / 64;
+                uint4 b[NT][2][2][2] = {};   // hi and lo
+                if (mine) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            if (n * 8 + g < T) {
-                                const int64_t at = ((int64_t)(n * 8 + g) * p.n_shared + ei) * (p.Ns / 8) + piece * 8 + h * 4 + t;
-                                bh[n][h] = __ldcg(reinterpret_cast<const uint4*>(p.act_hi) + at);
-                                bl[n][h] = __ldcg(reinterpret_cast<const uint4*>(p.act_lo) + at);
+                        for (int i = 0; i < 4; ++i)
+                            if (n * 8 + g < T && (i < 2 || p.rb.log > 0)) {
+                                const int64_t at = ((int64_t)(n * 8 + g) * p.n_shared + e) * (p.Ns / 8) + piece * 8 + i * 4 + t;
+                                b[n][0][i >> 1][i & 1] = __ldcg(reinterpret_cast<const uint4*>(p.act_hi) + at);
+                                b[n][1][i >> 1][i & 1] = __ldcg(reinterpret_cast<const uint4*>(p.act_lo) + at);
                             }
                 }
                 wait_full();
-                if (ok && live) {
-                    piece_mma_bf16<NT>(row, row + 1024, bh, acc);
-                    piece_mma_bf16<NT>(row, row + 1024, bl, acc);
+                if (ok && mine) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int pc = 0; pc < 2; ++pc) {
+                            if (pc && p.rb.log == 0) break;   // the unit has one piece
+#pragma unroll
+                            for (int part = 0; part < 2; ++part)
+                                piece_mma_bf16(base + row_off + pc * 2048, base + row_off + 1024 + pc * 2048, b[n][part][pc], acc[n]);
+                        }
                 }
             }
             release();
         }
-        const float* sums = share_sums(acc);
+        put_sums(0, acc);
+        consumers_sync();
         const bool whole = hi - lo == V;
         float* part = p.part + (int64_t)(tile + cta) * (128 * NT);   // tile + cta: its own for each (tile, CTA)
         float sum = 0.0f;
         const int s = threadIdx.x;
         if (s < 128 * NT)
-            for (int w = 0; w < kDecodeWarps; ++w) sum += sums[w * NT * 128 + s];
+            for (int w = 0; w < kDecodeWarps; ++w) sum += red[w * NT * 128 + s];
         if (!whole) {
             if (s < 128 * NT) part[s] = sum;
             __threadfence();
@@ -743,6 +905,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
             const int i = s >> 5, col = (i >> 2) * 8 + t * 2 + (i & 1), m = tile * 16 + g + 8 * ((i >> 1) & 1);
             if (col < T) p.out[(int64_t)col * p.H + m] = f32_to_bf16_bits(sum);
         }
+        consumers_sync();   // red is free for the next tile
         v += hi - lo;
     }
     if (!ok) give_up();
@@ -751,7 +914,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
 // ---- host ---------------------------------------------------------------------------------------
 
 struct DecodePlan {
-    size_t logits, h, hq, gs, act, part, count, total;
+    size_t logits, h, hq, gs, hsum, act, part, count, total;
 };
 
 inline DecodePlan plan_decode(const DecodeLayer& L, int64_t T, int k) {
@@ -767,6 +930,7 @@ inline DecodePlan plan_decode(const DecodeLayer& L, int64_t T, int k) {
     p.h = take(P * L.N * 4);
     p.hq = take(P * align_up(L.N, 256));
     p.gs = take(P * 4);
+    p.hsum = take(P * (align_up(L.N, 256) / 128) * 4);
     p.act = take((size_t)T * L.n_shared * L.shared_N * 4);     // hi, then lo
     p.part = take((size_t)(L.H / 16 + kDecodeMaxGrid) * 128 * nt * 4);
     p.count = take((size_t)(L.H / 16) * 4);
@@ -790,6 +954,7 @@ inline DecodeRows decode_rows(int64_t row_bytes, int log = -1) {
     r.pieces = static_cast<int>((row_bytes + 127) / 128);
     while (r.log < 4 && (1 << r.log) < r.pieces) ++r.log;
     if (log >= 0) r.log = log;
+    r.wlog = r.log > 0 ? r.log - 1 : 0;
     r.chunks = (r.pieces + (1 << r.log) - 1) >> r.log;
     return r;
 }
@@ -806,17 +971,19 @@ inline bool decode_map(CUtensorMap* m, const void* w, uint64_t row_bytes, uint64
 
 template <bool kMx, int NT>
 inline int launch_decode(DecodeParams& q, cudaStream_t stream) {
-    const size_t red = (size_t)kDecodeWarps * NT * 128 * 4;
-    const size_t scale_a = (size_t)(16 >> q.ra.log) * 16 * (kMx ? q.H / 32 : q.H / 64);
-    const size_t scale_b = (size_t)(16 >> q.rb.log) * 16 * (kMx ? q.N / 32 : q.N / 64);
+    const size_t scale_a = (size_t)(kDecodeWarps >> q.ra.wlog) * 16 * (kMx ? q.H / 32 : q.H / 64);
+    const size_t scale_b = (size_t)(kDecodeWarps >> q.rb.wlog) * 16 * (kMx ? q.N / 32 : q.N / 64);
     q.slot_bytes = static_cast<int>(align_up(kDecodeStage + std::max(scale_a, scale_b), 1024));
     const size_t frag = (size_t)((q.H + 255) / 256) * NT * kDecodePiece;
-    // 227 KB a CTA; long rows of two token blocks take one sum buffer so that two slots still fit
-    const size_t room = 227 * 1024 - sizeof(DecodeShared) - 1024 - 256 - frag;
-    q.red_bufs = room >= 2 * red + 3 * (size_t)q.slot_bytes ? 2 : 1;
-    q.slots = static_cast<int>(std::min<size_t>(kDecodeMaxSlots, (room - q.red_bufs * red) / q.slot_bytes));
+    const size_t room = 227 * 1024 - sizeof(DecodeShared) - 1024 - 256 - frag;   // of a CTA's 227 KB
+    size_t red = 0;
+    for (q.batch = kDecodeBatch; q.batch > 0; q.batch >>= 1) {   // fewer stages a sum where slots are short
+        red = (size_t)q.batch * kDecodeWarps * NT * 128 * 4;
+        q.slots = static_cast<int>(std::min<size_t>(kDecodeMaxSlots, (room - red) / q.slot_bytes));
+        if (q.slots >= 4 || q.batch == 1) break;
+    }
     if (q.slots < 2) return MOE_ERR_UNSUPPORTED_SHAPE;
-    const size_t smem = 1024 + (size_t)q.slots * q.slot_bytes + frag + q.red_bufs * red;
+    const size_t smem = 1024 + (size_t)q.slots * q.slot_bytes + frag + red;
     const void* fn = reinterpret_cast<const void*>(k_decode<kMx, NT>);
     if (set_smem(fn, smem)) return MOE_ERR_CUDA;
     int dev = 0, sms = 0;
@@ -875,6 +1042,7 @@ inline int decode_impl(const DecodeLayer& L, const uint16_t* x, const float* log
     q.h = reinterpret_cast<float*>(b + p.h);
     q.hq = b + p.hq;
     q.gs = reinterpret_cast<float*>(b + p.gs);
+    q.hsum = reinterpret_cast<float*>(b + p.hsum);
     q.act_hi = reinterpret_cast<uint16_t*>(b + p.act);
     q.act_lo = q.act_hi + (size_t)T * L.n_shared * L.shared_N;
     q.part = reinterpret_cast<float*>(b + p.part);

@@ -49,14 +49,11 @@
 namespace moe {
 
 constexpr int kDecodeMaxT = 16;
-constexpr int kDecodeWarps = 8;                          // consumer warps; one more streams the weights
-constexpr int kDecodeThreads = 32 * (kDecodeWarps + 1);
-constexpr int kDecodeStage = 32 * 1024;                  // weight bytes of a stage
+constexpr int kDecodeWarps = 8;                          // that multiply
+constexpr int kDecodeStreams = 4;                        // that stream the weights for them
+constexpr int kDecodeThreads = 32 * (kDecodeWarps + kDecodeStreams);
 constexpr int kDecodeMaxPairs = kDecodeMaxT * kMaxK;
-constexpr int kDecodeMaxSlots = 8;
-constexpr int kDecodeMaxGrid = 256;                      // CTAs the workspace's partial sums provide for
-constexpr int kDecodeBatch = 4;                          // phase A: most stages between two sums over the warps
-constexpr int kDecodePiece = 2048;                       // B-fragment bytes of 256 columns of eight tokens
+constexpr int kDecodeMaxSlots = 4;
 
 struct DecodeLayer {
     int E, H, N;
@@ -66,11 +63,10 @@ struct DecodeLayer {
     const uint16_t *sw[3];        // shared experts' gate, up, down (bf16)
 };
 
-// How rows of one weight matrix fill stages: `pieces` of 128 bytes a row.  A unit takes 1 << log of a
-// stage's 16 pieces in each of `chunks` stages, and 1 << wlog of the 8 consumer warps, two pieces a
-// warp (one where a row has no more); 8 >> wlog units share a stage.
+// Rows of one weight matrix: `pieces` of 128 bytes a row; a chunk is `cp` of them for the 16 rows of a
+// unit, a unit `chunks` chunks.
 struct DecodeRows {
-    int pieces, log, wlog, chunks;
+    int pieces, cp, chunks;
 };
 
 struct alignas(64) DecodeParams {
@@ -79,195 +75,187 @@ struct alignas(64) DecodeParams {
     const uint16_t *x, *wr;
     const float* logits;
     uint16_t* out;
-    float *h, *gs, *hsum, *part, *ws_logits;
+    float *h, *gs, *y, *hsum, *ws_logits;
     uint8_t* hq;
     uint16_t *act_hi, *act_lo;
-    unsigned* count;
-    DecodeRows ra, rs, rb;        // gate/up, shared gate/up, down (routed; its log serves the shared rows too)
-    int shared_chunks;            // stages' worth of a shared down row
+    DecodeRows rows[4];           // gate/up, shared gate/up, down, shared down
     int E, H, N, k, T, n_shared, Ns;
-    int slots, slot_bytes, batch, flat;   // flat: bit i set, map i is 2-D (rows are not whole pieces)
+    int slots, slot_bytes, scale_bytes;   // scale_bytes: of one of a warp's `slots` scale buffers, 0: read in place
+    int flat;                     // bit i set: map i is 2-D (rows are not whole pieces)
 };
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1, float c0, float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    mma_f16(d, a0, a1, a2, a3, b0, b1, d[0], d[1], d[2], d[3]);
 }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ float lds_bf16(uint32_t a) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-    return bf16_bits_to_f32(v);
-}
+// Shared memory by its offset in the dynamic array (plain loads: the compiler may move them between barriers).
+extern __shared__ __align__(16) uint8_t g_decode_smem[];
+__device__ __forceinline__ uint4 lds128(uint32_t a) { return *reinterpret_cast<const uint4*>(g_decode_smem + a); }
+__device__ __forceinline__ uint32_t lds32(uint32_t a) { return *reinterpret_cast<const uint32_t*>(g_decode_smem + a); }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// Two E8M0 bytes (the low half of b) -> two floats.
-__device__ __forceinline__ float2 e8m0x2_to_f32(uint32_t b) {
-    const __nv_bfloat162_raw r = __nv_cvt_e8m0x2_to_bf162raw(static_cast<__nv_fp8x2_storage_t>(b & 0xFFFFu));
-    return make_float2(bf16_bits_to_f32(r.x), bf16_bits_to_f32(r.y));
+// Row g of an MMA's eight is row lane_row() of the eight in shared memory: eight consecutive lanes (two g) then
+// read rows whose swizzle differs in bit 2, so a 16-byte load of four neighbouring chunks of each has no bank conflict.
+__device__ __forceinline__ int lane_row(int g) { return (g >> 1) | ((g & 1) << 2); }
+// Four E8M0 bytes -> four floats.
+__device__ __forceinline__ void e8m0x4_to_f32(uint32_t b, float (&s)[4]) {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 h0, h1;\n\tmov.b32 {h0, h1}, %2;\n\tcvt.rn.bf16x2.ue8m0x2 %0, h0;\n\tcvt.rn.bf16x2.ue8m0x2 %1, h1;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(b));
+    s[0] = __uint_as_float(lo << 16);
+    s[1] = __uint_as_float(lo & 0xFFFF0000u);
+    s[2] = __uint_as_float(hi << 16);
+    s[3] = __uint_as_float(hi & 0xFFFF0000u);
+}
+// Eight E2M1 codes -> four f16x2 in order.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\tcvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
 }
 
-// Where the FP8 codes of columns 8 c8 .. 8 c8 + 7 lie in a token's row of B fragments: pieces of
-// 256 columns; lane (token, t) reads its 64 bytes of a piece as four 16-byte words i = 2 h + j / 2, each
-// the codes of weight words j and j + 1 of half h.  Word j of lane t covers columns 32 t + 8 j (INT4:
-// a lane's 16 bytes of a weight row) or 32 j + 8 t (MXFP4: one block a word of the lanes) of the half.
-template <bool kMx>
-__device__ __forceinline__ void frag_place(int c8, int& piece, int& i, int& t, int& odd) {
-    const int idx = c8 & 15, h = (c8 >> 4) & 1;
-    const int j = kMx ? idx >> 2 : idx & 3;
-    t = kMx ? idx & 3 : idx >> 2;
-    piece = c8 >> 5;
-    i = 2 * h + (j >> 1);
-    odd = j & 1;
-}
 // Eight codes in column order -> the order in which the weights' widening pairs them: for INT4 the
 // nibbles of a word come out as (0,4) (1,5) (2,6) (3,7), for MXFP4 as they are.
 template <bool kMx>
 __device__ __forceinline__ uint2 frag_order(uint2 c) {
     return kMx ? c : make_uint2(__byte_perm(c.x, c.y, 0x5140), __byte_perm(c.x, c.y, 0x7362));
 }
-// Four codes in that order -> the two B registers of one MMA.
+// Eight codes in that order -> the B registers of two MMAs.
 template <bool kMx>
-__device__ __forceinline__ void frag_f16(uint32_t c, uint32_t& b0, uint32_t& b1) {
-    const __half2_raw l = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c & 0xFFFFu), __NV_E4M3);
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c >> 16), __NV_E4M3);
-    b0 = *reinterpret_cast<const uint32_t*>(&l);
-    b1 = *reinterpret_cast<const uint32_t*>(&h);
-    if constexpr (!kMx) {   // the nibbles in bits 4..7 stand for 16 n
-        const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h), __half2half2(__ushort_as_half(0x2C00)));   // 2^-4
-        b1 = *reinterpret_cast<const uint32_t*>(&v);
+__device__ __forceinline__ uint4 frag_f16(uint2 c) {
+    uint4 r;
+    asm("{\n\t.reg .b16 h0, h1, h2, h3;\n\tmov.b32 {h0, h1}, %4;\n\tmov.b32 {h2, h3}, %5;\n\tcvt.rn.f16x2.e4m3x2 %0, h0;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h1;\n\tcvt.rn.f16x2.e4m3x2 %2, h2;\n\tcvt.rn.f16x2.e4m3x2 %3, h3;\n\t}"
+        : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(c.x), "r"(c.y));
+    if constexpr (!kMx) {   // the nibbles in bits 4..7 stand for 16 n: 2^-4
+        const __half2 m = __half2half2(__ushort_as_half(0x2C00));
+        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&r.y), m), w = __hmul2(*reinterpret_cast<const __half2*>(&r.w), m);
+        r.y = *reinterpret_cast<const uint32_t*>(&y);
+        r.w = *reinterpret_cast<const uint32_t*>(&w);
     }
+    return r;
 }
+// A token's (or pair's) row of B fragments: pieces of 256 columns; in a piece, word i = 4 h + j of lane t
+// holds the eight columns that word j of the lane's weights in half h covers: 32 t + 8 j (INT4: a lane
+// reads 16 bytes of a weight row at once) or 32 j + 8 t (MXFP4: the lanes' words j are one block).  As
+// f16 a word is 16 bytes at 64 i + 16 t, as FP8 8 bytes at 64 (i / 2) + 16 t + 8 (i % 2).
+template <bool kMx>
+__device__ __forceinline__ void frag_place(int c8, int& piece, int& i, int& t) {
+    const int idx = c8 & 15, j = kMx ? idx >> 2 : idx & 3;
+    t = kMx ? idx & 3 : idx >> 2;
+    piece = c8 >> 5;
+    i = 4 * ((c8 >> 4) & 1) + j;
+}
+
 constexpr float kNibbleOffset = -8.0f / 16777216.0f;   // -8 2^-24
-
-// A warp's B fragments of one block of eight tokens: the 512 columns of its two pieces as f16 (four
-// halves of 128 columns), from the FP8 codes.
-template <bool kMx>
-__device__ __forceinline__ void frags_f16(const uint4 (&q)[8], uint32_t (&f)[64]) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) frag_f16<kMx>(word(q[i >> 2], i & 3), f[2 * i], f[2 * i + 1]);
-}
-// INT4: where the accumulators start, off[h] = -8 2^-24 sum_q over half h, for the lane's two
-// token columns.
-__device__ __forceinline__ void nibble_offsets(const uint32_t (&f)[64], float2 (&off)[4]) {
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-        float p[4] = {};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)   // -8 2^-24, -8 2^-20
-            mma_f16(p, 0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u, f[16 * h + 2 * i], f[16 * h + 2 * i + 1]);
-        off[h] = make_float2(p[0], p[1]);
-    }
-}
-
-// Two E2M1 codes (the low byte of c) -> f16x2, the low nibble first.
-__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t c) {
-    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(c & 0xFFu), __NV_E2M1);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// acc += the products of 16 rows x 512 weights (two pieces, `step` bytes apart in the stage) with the
-// B fragments of one block of tokens.  row_a / row_b: the lane's rows g and g + 8; sa / sb: those
-// rows' scales at the first piece; halves: how many of the four 128-column halves lie inside the row
-// (a missing one has fragments and offsets of zero, and its scale is taken as nothing).  Nothing
-// branches, so the halves' loads and MMA chains overlap.
-template <bool kMx>
-__device__ __forceinline__ void pieces_mma(uint32_t row_a, uint32_t row_b, uint32_t step, uint32_t sa, uint32_t sb,
-                                           int halves, const uint32_t (&f)[64], const float2 (&off)[4], float (&acc)[4]) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    if constexpr (!kMx) {
-        const uint32_t at0 = (t ^ g) << 4;
-        float s0[4], s1[4];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            s0[h] = h < halves ? lds_bf16(sa + 2 * h) : 0.0f;
-            s1[h] = h < halves ? lds_bf16(sb + 2 * h) : 0.0f;
-        }
-#pragma unroll
-        for (int pc = 0; pc < 2; ++pc) {
-            uint4 wa[2], wb[2];
-            float p[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                wa[h] = lds128(row_a + pc * step + (at0 ^ (h * 64)));
-                wb[h] = lds128(row_b + pc * step + (at0 ^ (h * 64)));
-                p[h][0] = p[h][2] = off[2 * pc + h].x;
-                p[h][1] = p[h][3] = off[2 * pc + h].y;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t a = word(wa[h], j) >> (8 * s), c = word(wb[h], j) >> (8 * s);
-                        const int i = 16 * (2 * pc + h) + 4 * j + 2 * s;
-                        mma_f16(p[h], a & 0x000F000Fu, c & 0x000F000Fu, a & 0x00F000F0u, c & 0x00F000F0u, f[i], f[i + 1]);
-                    }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                acc[0] = fmaf(s0[2 * pc + h], p[h][0], acc[0]);
-                acc[1] = fmaf(s0[2 * pc + h], p[h][1], acc[1]);
-                acc[2] = fmaf(s1[2 * pc + h], p[h][2], acc[2]);
-                acc[3] = fmaf(s1[2 * pc + h], p[h][3], acc[3]);
-            }
-        }
-    } else {
-        uint32_t ea[4], eb[4];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            ea[h] = h < halves ? lds32(sa + 4 * h) : 0u;
-            eb[h] = h < halves ? lds32(sb + 4 * h) : 0u;
-        }
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t at = (h >> 1) * step + ((((h & 1) * 4 + j) ^ g) << 4) + 4 * t;
-                const uint32_t a = lds32(row_a + at), c = lds32(row_b + at);
-                const float2 e0 = e8m0x2_to_f32(ea[h] >> (16 * (j >> 1))), e1 = e8m0x2_to_f32(eb[h] >> (16 * (j >> 1)));
-                const float f0 = j & 1 ? e0.y : e0.x, f1 = j & 1 ? e1.y : e1.x;
-                float p[4] = {};
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int i = 16 * h + 4 * j + 2 * s;
-                    mma_f16(p, e2m1x2_to_f16x2(a >> (16 * s)), e2m1x2_to_f16x2(c >> (16 * s)),
-                            e2m1x2_to_f16x2(a >> (16 * s + 8)), e2m1x2_to_f16x2(c >> (16 * s + 8)), f[i], f[i + 1]);
-                }
-                acc[0] = fmaf(f0, p[0], acc[0]);
-                acc[1] = fmaf(f0, p[1], acc[1]);
-                acc[2] = fmaf(f1, p[2], acc[2]);
-                acc[3] = fmaf(f1, p[3], acc[3]);
-            }
-    }
-}
-// The power of two that pieces_mma's sums lack.
+// The power of two that the routed products' sums lack.
 template <bool kMx>
 constexpr float kDecodeLadder = kMx ? 1.0f : 16777216.0f;
 
-// The same for 16 rows x 64 bf16 weights of one piece and one block of tokens; b: the lane's eight
-// values of each half (32 columns).
+// A lane's scales (rows g and g + 8) of a piece, from the rows' scales in shared memory (offsets) or, where
+// the buffers do not fit, in place.
+template <bool kSmem>
+struct DecodeScales {
+    using At = std::conditional_t<kSmem, uint32_t, const uint8_t*>;
+    At a, b;
+    template <class V>
+    static __device__ __forceinline__ V load(At at) {
+        if constexpr (kSmem) return *reinterpret_cast<const V*>(g_decode_smem + at);
+        else return __ldg(reinterpret_cast<const V*>(at));
+    }
+    __device__ __forceinline__ void int4(int halves, float (&s0)[2], float (&s1)[2]) const {
+        const uint32_t second = halves > 1 ? 2 : 0;   // (the first again: its sums are dropped)
+        s0[0] = bf16_bits_to_f32(load<uint16_t>(a));
+        s1[0] = bf16_bits_to_f32(load<uint16_t>(b));
+        s0[1] = bf16_bits_to_f32(load<uint16_t>(a + second));
+        s1[1] = bf16_bits_to_f32(load<uint16_t>(b + second));
+    }
+    __device__ __forceinline__ void mx(int h, float (&s0)[4], float (&s1)[4]) const {
+        e8m0x4_to_f32(load<uint32_t>(a + 4 * h), s0);
+        e8m0x4_to_f32(load<uint32_t>(b + 4 * h), s1);
+    }
+};
+
+// acc += the products of one piece (16 rows x 256 weights) with the B fragments f of eight token
+// columns.  row_a / row_b: the lane's rows g and g + 8; sa / sb: those rows' scales at the piece;
+// halves: 1 when only the first 128 columns lie inside the row.  off: INT4, where the accumulators of
+// the lane's two columns start, by half: -8 2^-24 sum q.
+template <bool kMx, class Scales>
+__device__ __forceinline__ void piece_mma(uint32_t row_a, uint32_t row_b, const Scales& sc, int halves,
+                                          const uint4 (&f)[8], float2 off0, float2 off1, float (&acc)[4]) {
+    const int lane = threadIdx.x & 31, g = lane_row(lane >> 2), t = lane & 3;
+    if constexpr (!kMx) {
+        const uint32_t at0 = (t ^ g) << 4;
+        uint4 wa[2], wb[2];
+        float p[2][2][4], s0[2], s1[2];   // [half][word parity]: four independent chains
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            wa[h] = lds128(row_a + (at0 ^ (h * 64)));
+            wb[h] = lds128(row_b + (at0 ^ (h * 64)));
+        }
+        sc.int4(halves, s0, s1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t a = word(wa[h], j) >> (8 * s), c = word(wb[h], j) >> (8 * s);
+                    const uint32_t a0 = a & 0x000F000Fu, a1 = c & 0x000F000Fu, a2 = a & 0x00F000F0u, a3 = c & 0x00F000F0u;
+                    const uint32_t b0 = s ? f[4 * h + j].z : f[4 * h + j].x, b1 = s ? f[4 * h + j].w : f[4 * h + j].y;
+                    const float2 o = h ? off1 : off0;   // (columns 2 t and 2 t + 1)
+                    if (j == 0 && s == 0) mma_f16(p[h][0], a0, a1, a2, a3, b0, b1, o.x, o.y, o.x, o.y);
+                    else if (j == 1 && s == 0) mma_f16(p[h][1], a0, a1, a2, a3, b0, b1, 0.0f, 0.0f, 0.0f, 0.0f);
+                    else mma_f16(p[h][j & 1], a0, a1, a2, a3, b0, b1);
+                }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (h && halves < 2) break;
+            acc[0] = fmaf(s0[h], p[h][0][0] + p[h][1][0], acc[0]);
+            acc[1] = fmaf(s0[h], p[h][0][1] + p[h][1][1], acc[1]);
+            acc[2] = fmaf(s1[h], p[h][0][2] + p[h][1][2], acc[2]);
+            acc[3] = fmaf(s1[h], p[h][0][3] + p[h][1][3], acc[3]);
+        }
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (h && halves < 2) break;
+            float s0[4], s1[4];
+            sc.mx(h, s0, s1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t at = (((h * 4 + j) ^ g) << 4) + 4 * t;
+                uint32_t a[4], c[4];
+                e2m1x8_to_f16(lds32(row_a + at), a);
+                e2m1x8_to_f16(lds32(row_b + at), c);
+                const uint4& q = f[4 * h + j];
+                float p[4];
+                mma_f16(p, a[0], c[0], a[1], c[1], q.x, q.y, 0.0f, 0.0f, 0.0f, 0.0f);
+                mma_f16(p, a[2], c[2], a[3], c[3], q.z, q.w);
+                acc[0] = fmaf(s0[j], p[0], acc[0]);
+                acc[1] = fmaf(s0[j], p[1], acc[1]);
+                acc[2] = fmaf(s1[j], p[2], acc[2]);
+                acc[3] = fmaf(s1[j], p[3], acc[3]);
+            }
+        }
+    }
+}
+
+// The same for 16 rows x 64 bf16 weights of one piece; b: the lane's eight values of each half (32 columns).
 __device__ __forceinline__ void piece_mma_bf16(uint32_t row_a, uint32_t row_b, const uint4 (&b)[2], float (&acc)[4]) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int lane = threadIdx.x & 31, g = lane_row(lane >> 2), t = lane & 3;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const uint32_t at = ((h * 4 + t) ^ g) << 4;
@@ -296,7 +284,18 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kDecodeWarps) : "memory"); }
+// Whether the phase of the given parity has completed (returns at once).
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(tc::smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+constexpr int kMul = 32 * kDecodeWarps;   // threads that multiply
+__device__ __forceinline__ void multipliers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kMul) : "memory"); }
 
 // The first unit of CTA c's even share of n units.
 __device__ __forceinline__ int share(int n, int c, int G) { return static_cast<int>((int64_t)n * c / G); }
@@ -336,6 +335,36 @@ __device__ __forceinline__ void rank_row(const float* l, int E, int k, int* ids,
     if (lane < k) gates[lane] = __fdiv_rn(mine, sum);
 }
 
+// The FP8 codes of a row whose largest magnitude is amax: e4m3(x / s) with s = amax / 448, the quotients rounded as
+// IEEE division rounds them: q = RN(x r), r = RN(1 / s), then q + r (x - q s) with the remainder exact in an fma
+// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).  That needs r
+// normal and remainders that do not underflow where they matter; rows outside [2^-60, 2^60] divide plainly.
+struct RowQuant {
+    float s, r;
+    bool plain;
+    static __device__ __forceinline__ RowQuant of(float amax) {
+        RowQuant q;
+        q.s = __fdiv_rn(amax, kFp8Max);
+        q.plain = !(q.s >= 0x1p-60f && q.s <= 0x1p60f);
+        q.r = q.plain ? 0.0f : __frcp_rn(q.s);
+        return q;
+    }
+    __device__ __forceinline__ float divide(float x) const {
+        const float q = x * r;
+        return fmaf(fmaf(-q, s, x), r, q);
+    }
+    __device__ __forceinline__ uint2 codes(const float (&x)[8]) const {
+        uint2 c = make_uint2(0u, 0u);
+        if (s == 0.0f) return c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = plain ? __fdiv_rn(x[2 * i], s) : divide(x[2 * i]), b = plain ? __fdiv_rn(x[2 * i + 1], s) : divide(x[2 * i + 1]);
+            (i < 2 ? c.x : c.y) |= static_cast<uint32_t>(f32x2_to_e4m3x2(a, b)) << (16 * (i & 1));
+        }
+        return c;
+    }
+};
+
 // A wait ran out: the status word is set, and the warp stays until its CTA's copies in flight (microseconds) have landed.
 __device__ __forceinline__ void give_up() {
     if ((threadIdx.x & 31) == 0) atomicOr(&g_device_status, kStatusTimeout);
@@ -344,119 +373,359 @@ __device__ __forceinline__ void give_up() {
 }
 
 struct DecodeShared {
-    uint64_t full[kDecodeMaxSlots], empty[kDecodeMaxSlots];
+    uint64_t full[kDecodeWarps][kDecodeMaxSlots], empty[kDecodeWarps][kDecodeMaxSlots];
     int ids[kDecodeMaxPairs];
     float gates[kDecodeMaxPairs], gs[kDecodeMaxPairs];
     int expert[kDecodeMaxPairs];                     // the touched experts, ascending
     uint32_t tokens[kDecodeMaxPairs];                // bit t: token t is routed to it
-    int8_t pick[kDecodeMaxPairs][kDecodeMaxT];       // as its which selection
+    uint8_t list[kDecodeMaxPairs][kDecodeMaxT];      // those tokens, ascending
+    uint8_t pair[kDecodeMaxPairs][kDecodeMaxT];      // and their pairs t k + j
     uint32_t bitmap[kMaxE / 32];
     unsigned amax[kDecodeMaxT];
-    float red[32];
-    int n_experts, last;
+    float sx[kDecodeMaxT];
+    float red[(kDecodeWarps + kDecodeStreams) * kDecodeMaxT];
+    int first[4], end[4], per_expert[4];             // this CTA's units of each phase, and how many an expert has
+    int need[kDecodeMaxT], n_need;
+    int n_experts;
     volatile int abort;
 };
 
-// A stage ring's position, as the producer and the consumers count it.
-struct DecodeRing {
-    int slot = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next(int slots) {
-        if (++slot == slots) { slot = 0; phase ^= 1u; }
+// A lane of a streaming warp: it loads for multiplying warp `to`, chunk after chunk of the warp's sequence: phases 0 gate/up,
+// 1 shared gate/up, 2 down, 3 shared down; in a phase every kDecodeWarps-th of the CTA's units; a unit's chunks.
+template <bool kMx>
+struct DecodeStream {
+    const DecodeParams& p;
+    DecodeShared& S;
+    int to;
+    uint32_t slots0, scales0;                 // shared-memory addresses of the warp's slots and scale buffers
+    int ph = 0, u = 0, c = 0, e = 0, b = 0;   // unit u is the b-th of expert (place) e
+    int slot = 0, buf = 0;                    // ring slot; scale buffer of the unit
+    uint32_t parity = 1;
+    int ahead = 0;                            // chunks of the down phases issued
+    bool ok = true;
+
+    // Enters phase n, or the next in which the warp has units (4: none).
+    __device__ __forceinline__ void enter(int n) {
+        while (n < 4 && S.first[n] + to >= S.end[n]) ++n;
+        ph = n;
+        if (n < 4) {
+            u = S.first[n] + to;
+            e = u / S.per_expert[n];
+            b = u - e * S.per_expert[n];
+        }
+    }
+    __device__ __forceinline__ void issue() {
+        const bool sh = ph & 1, down = ph >= 2;
+        const DecodeRows R = p.rows[ph];
+        const int per = down ? 16 : 8;
+        const int row = (sh ? e : S.expert[e]) * (down ? p.H : sh ? p.Ns : p.N) + b * per;
+        const int K = down ? p.N : p.H;
+        const uint32_t rs = kMx ? K / 32 : K / 64, bytes = per * rs;
+        const bool scales = !sh && c == 0 && p.scale_bytes;
+        uint64_t* bar = &S.full[to][slot];
+        tc::mbar_arrive_expect_tx(bar, 2048u * R.cp + (scales ? 16u * rs : 0u));
+        const uint32_t dst = slots0 + slot * p.slot_bytes;
+        for (int i = 0; i < (down ? 1 : 2); ++i) {
+            const int m = (sh ? 3 : 0) + (down ? 2 : i);
+            if (!((p.flat >> m) & 1)) {
+                tma_load_3d(dst + i * (1024u * R.cp), &p.map[m], 0, row, c * R.cp, bar);
+            } else {
+                for (int x = 0; x < R.cp; ++x)
+                    tma_load_2d_at(dst + i * (1024u * R.cp) + x * per * 128, &p.map[m], (c * R.cp + x) * 128, row, bar);
+            }
+            if (scales) bulk_load(scales0 + buf * p.scale_bytes + i * bytes, p.scale[down ? 2 : i] + (int64_t)row * rs, bytes, bar);
+        }
+        ahead += down;
+        if (++slot == p.slots) { slot = 0; parity ^= 1u; }
+        if (++c < R.chunks) return;
+        c = 0;
+        if (++buf == p.slots) buf = 0;
+        u += kDecodeWarps;
+        if (u >= S.end[ph]) {
+            enter(ph + 1);
+        } else {
+            b += kDecodeWarps;
+            for (const int n = S.per_expert[ph]; b >= n; b -= n) ++e;
+        }
+    }
+    // Issues until every lane is through, or (up_to_barrier) as far into the down phases as the slots reach.
+    __device__ __forceinline__ void run(bool up_to_barrier) {
+        uint64_t t0 = 0;
+        for (uint32_t n = 1;; ++n) {
+            const bool active = ok && ph < 4 && !(up_to_barrier && ahead >= p.slots);
+            if (!__any_sync(0xffffffffu, active)) return;
+            const bool ready = active && mbar_test_wait(&S.empty[to][slot], parity);
+            if (ready) issue();
+            if (__any_sync(0xffffffffu, ready)) {
+                t0 = 0;
+                continue;
+            }
+            __nanosleep(20);
+            if (t0 == 0) t0 = tc::globaltimer_ns();
+            else if ((n & 255) == 0 && (S.abort || tc::globaltimer_ns() - t0 > 2000000000ull)) { S.abort = 1; ok = false; }
+        }
     }
 };
 
-template <bool kMx, int NT>
+// A multiplying warp.
+template <bool kMx, bool kF8, bool kScaleSmem>
+struct DecodeWarp {
+    const DecodeParams& p;
+    DecodeShared& S;
+    int warp, lane, g, t, r;                        // r: the lane's row
+    uint32_t slots0, scales0, frags, xsum;          // offsets in the dynamic shared memory; slots0, scales0: the warp's
+    int slot = 0, buf = 0;
+    uint32_t parity = 0;
+    bool ok = true;
+
+    __device__ __forceinline__ void wait_full() { ok = ok && ws::wait(&S.full[warp][slot], parity, &S.abort); }
+    __device__ __forceinline__ void release() {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&S.empty[warp][slot]);
+        if (++slot == p.slots) { slot = 0; parity ^= 1u; }
+    }
+    template <bool kDown>
+    __device__ __forceinline__ void routed();
+    template <bool kDown>
+    __device__ __forceinline__ void shared();
+};
+
+template <bool kMx, bool kF8, bool kScaleSmem>
+template <bool kDown>
+__device__ __forceinline__ void DecodeWarp<kMx, kF8, kScaleSmem>::routed() {
+    constexpr int ph = kDown ? 2 : 0;
+    const DecodeRows R = p.rows[ph];
+    const int K = kDown ? p.N : p.H, pieces = (K + 255) / 256, per = S.per_expert[ph], end = S.end[ph];
+    const uint32_t rs = kMx ? K / 32 : K / 64, step = kDown ? 2048 : 1024, row_b = kDown ? 1024u : 1024u * R.cp;
+    const uint32_t frag_row = pieces * (kF8 && !kDown ? 256 : 512);
+    for (int u = S.first[ph] + warp; u < end; u += kDecodeWarps) {
+        const int e = u / per, b = u - e * per, n_tok = __popc(S.tokens[e]);
+        const uint8_t* of = kDown ? S.pair[e] : S.list[e];   // the columns' pairs (tokens)
+        const int col = 2 * t;                               // the lane's accumulators' first column of a block
+        DecodeScales<kScaleSmem> sc;
+        if constexpr (kScaleSmem) {
+            sc.a = scales0 + buf * p.scale_bytes + r * rs;
+            sc.b = sc.a + 8 * rs;
+            if (++buf == p.slots) buf = 0;
+        } else {
+            const int64_t row = (int64_t)S.expert[e] * (kDown ? p.H : p.N) + b * (kDown ? 16 : 8) + r;
+            sc.a = p.scale[kDown ? 2 : 0] + row * rs;
+            sc.b = kDown ? sc.a + 8 * rs : p.scale[1] + row * rs;
+        }
+        // an unused column takes its block's first token: the loads coincide, and nobody reads its sums
+        auto column = [&](int n, int i) { return (int)of[8 * n + i < n_tok ? 8 * n + i : 8 * n]; };
+        const int who0 = column(0, g), c00 = kMx ? 0 : column(0, col), c01 = kMx ? 0 : column(0, col + 1);
+        float acc[2][4] = {};
+        for (int c = 0; c < R.chunks; ++c) {
+            wait_full();
+            const int first = c * R.cp, last = min(first + R.cp, R.pieces);
+#pragma unroll 1
+            for (int n = 0; ok && 8 * n < n_tok; ++n) {      // blocks of eight columns: nearly always one
+                const int who = n ? column(1, g) : who0;
+                const uint32_t at = frags + who * frag_row + t * 16;
+                const uint8_t* src = kDown ? p.hq + who * (int64_t)frag_row + t * 16 : nullptr;
+                uint32_t o0 = 0, o1 = 0;                     // group sums of the lane's two columns
+                if constexpr (!kMx) {
+                    o0 = (n ? column(1, col) : c00) * pieces;
+                    o1 = (n ? column(1, col + 1) : c01) * pieces;
+                }
+                uint32_t row = slots0 + slot * p.slot_bytes + r * 128;
+                float a[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = n ? acc[1][i] : acc[0][i];
+#pragma unroll 1
+                for (int piece = first; piece < last; ++piece, row += step) {
+                    uint4 f[8];
+                    if constexpr (kDown) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[i] = *reinterpret_cast<const uint4*>(src + piece * 512 + i * 64);
+                    } else if constexpr (kF8) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 v = lds128(at + piece * 256 + ((i ^ (who & 3)) * 64));
+                            f[2 * i] = frag_f16<kMx>(make_uint2(v.x, v.y));
+                            f[2 * i + 1] = frag_f16<kMx>(make_uint2(v.z, v.w));
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[i] = lds128(at + piece * 512 + ((i ^ (who & 7)) * 64));
+                    }
+                    float2 off0 = {}, off1 = {};
+                    if constexpr (!kMx) {
+                        float2 x, y;
+                        if constexpr (kDown) {
+                            x = reinterpret_cast<const float2*>(p.hsum)[o0 + piece];
+                            y = reinterpret_cast<const float2*>(p.hsum)[o1 + piece];
+                        } else {
+                            x = *reinterpret_cast<const float2*>(g_decode_smem + xsum + (o0 + piece) * 8);
+                            y = *reinterpret_cast<const float2*>(g_decode_smem + xsum + (o1 + piece) * 8);
+                        }
+                        off0 = make_float2(x.x, y.x);
+                        off1 = make_float2(x.y, y.y);
+                    }
+                    const DecodeScales<kScaleSmem> s{sc.a + piece * (kMx ? 8 : 4), sc.b + piece * (kMx ? 8 : 4)};
+                    piece_mma<kMx>(row, row + row_b, s, K / 128 - 2 * piece, f, off0, off1, a);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[0][i] = n ? acc[0][i] : a[i];
+                    acc[1][i] = n ? a[i] : acc[1][i];
+                }
+            }
+            release();
+        }
+        // outputs: the lane's rows and its two token columns
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int c1 = 0; c1 < 2; ++c1) {
+                if (8 * n + col + c1 >= n_tok) continue;
+                const int pr = S.pair[e][8 * n + col + c1];
+                if constexpr (kDown) {
+                    p.y[(int64_t)pr * p.H + b * 16 + r] = acc[n][c1] * S.gs[pr];
+                    p.y[(int64_t)pr * p.H + b * 16 + r + 8] = acc[n][c1 + 2] * S.gs[pr];
+                } else {
+                    const float sx = S.sx[S.list[e][8 * n + col + c1]];
+                    p.h[(int64_t)pr * p.N + b * 8 + r] = silu(acc[n][c1] * sx) * (acc[n][c1 + 2] * sx);
+                }
+            }
+    }
+}
+
+template <bool kMx, bool kF8, bool kScaleSmem>
+template <bool kDown>
+__device__ __forceinline__ void DecodeWarp<kMx, kF8, kScaleSmem>::shared() {   // bf16 weights, every token
+    constexpr int ph = kDown ? 3 : 1;
+    const DecodeRows R = p.rows[ph];
+    const int per = S.per_expert[ph], end = S.end[ph];
+    const uint32_t step = kDown ? 2048 : 1024, row_b = kDown ? 1024u : 1024u * R.cp;
+    for (int u = S.first[ph] + warp; u < end; u += kDecodeWarps) {
+        const int e = u / per, b = u - e * per;
+        float acc[2][4] = {};
+        for (int c = 0; c < R.chunks; ++c) {
+            wait_full();
+            const int first = c * R.cp, last = min(first + R.cp, R.pieces);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                if (8 * n >= p.T || !ok) break;
+                const int tk = min(8 * n + g, p.T - 1);      // (an unused column takes the last token's)
+                uint32_t row = slots0 + slot * p.slot_bytes + r * 128;
+#pragma unroll 2
+                for (int piece = first; piece < last; ++piece, row += step) {
+                    uint4 v[kDown ? 2 : 1][2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if constexpr (kDown) {
+                            const int64_t at = ((int64_t)tk * p.n_shared + e) * (p.Ns / 8) + piece * 8 + h * 4 + t;
+                            v[0][h] = reinterpret_cast<const uint4*>(p.act_hi)[at];
+                            v[1][h] = reinterpret_cast<const uint4*>(p.act_lo)[at];
+                        } else {
+                            v[0][h] = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)tk * p.H) + piece * 8 + h * 4 + t);
+                        }
+                    }
+#pragma unroll
+                    for (int part = 0; part < (kDown ? 2 : 1); ++part) piece_mma_bf16(row, row + row_b, v[part], acc[n]);
+                }
+            }
+            release();
+        }
+        if (++buf == p.slots) buf = 0;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int c1 = 0; c1 < 2; ++c1) {
+                const int tk = 8 * n + 2 * t + c1;
+                if (tk >= p.T) continue;
+                if constexpr (kDown) {
+                    float* y = p.y + ((int64_t)p.T * p.k + e * p.T + tk) * p.H + b * 16 + r;
+                    y[0] = acc[n][c1];
+                    y[8] = acc[n][c1 + 2];
+                } else {
+                    const float a = silu(acc[n][c1]) * acc[n][c1 + 2];
+                    const uint16_t hi = f32_to_bf16_bits(a);   // hi + lo: 16 bits of the activation
+                    const int64_t at = ((int64_t)tk * p.n_shared + e) * p.Ns + b * 8 + r;
+                    p.act_hi[at] = hi;
+                    p.act_lo[at] = f32_to_bf16_bits(a - bf16_bits_to_f32(hi));
+                }
+            }
+    }
+}
+
+template <bool kMx, bool kF8, bool kScaleSmem>
 __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_constant__ DecodeParams p) {
     namespace cg = cooperative_groups;
-    extern __shared__ uint8_t smem_raw[];
     __shared__ DecodeShared S;
-    const uint32_t ring = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t frags = ring + p.slots * p.slot_bytes;               // B fragments of the tokens
-    const uint32_t frag_bytes = ((p.H + 255) / 256) * NT * kDecodePiece;
-    float* red = reinterpret_cast<float*>(smem_raw + (frags + frag_bytes - tc::smem_u32(smem_raw)));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t smem0 = tc::smem_u32(g_decode_smem);
+    const uint32_t ring = ((smem0 + 1023u) & ~1023u) - smem0;           // offsets in the dynamic shared memory
+    const uint32_t scales = ring + kDecodeWarps * p.slots * p.slot_bytes;
+    const uint32_t frags = scales + kDecodeWarps * p.slots * p.scale_bytes;
+    const int pieces_x = (p.H + 255) / 256, pieces_h = (p.N + 255) / 256;
+    const uint32_t xsum = frags + p.T * pieces_x * (kF8 ? 256 : 512);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = gridDim.x, cta = blockIdx.x;
     const int T = p.T, k = p.k, P = T * k;
-    const bool producer = warp == kDecodeWarps;
 
     // ---- prologue ----
     if (threadIdx.x == 0) {
-        for (int i = 0; i < p.slots; ++i) {
-            tc::mbar_init(&S.full[i], 1);
-            tc::mbar_init(&S.empty[i], kDecodeWarps);
+        for (int i = 0; i < kDecodeWarps * p.slots; ++i) {
+            tc::mbar_init(&S.full[i / p.slots][i % p.slots], 1);
+            tc::mbar_init(&S.empty[i / p.slots][i % p.slots], 1);
         }
         tc::fence_mbar_init();
         S.abort = 0;
     }
-    if (producer && lane < (p.n_shared ? 6 : 3)) ws::prefetch_map(&p.map[lane]);
+    if (warp == 1 && lane < (p.n_shared ? 6 : 3)) ws::prefetch_map(&p.map[lane]);
     for (int i = threadIdx.x; i < kMaxE / 32; i += kDecodeThreads) S.bitmap[i] = 0u;
     for (int i = threadIdx.x; i < kDecodeMaxPairs; i += kDecodeThreads) S.tokens[i] = 0u;
     if (threadIdx.x < kDecodeMaxT) S.amax[threadIdx.x] = 0u;
-    const int tiles = p.H / 16;
-    for (int i = cta * kDecodeThreads + threadIdx.x; i < tiles; i += G * kDecodeThreads) p.count[i] = 0u;
     __syncthreads();
 
-    // max |x| of the tokens: 8 / (T rounded up to a power of two) warps a token
-    const int twarps = kDecodeWarps >> (T > 4 ? 3 : T > 2 ? 2 : T > 1 ? 1 : 0);
-    const int tok0 = warp / twarps, tpart = warp % twarps;
-    if (!producer) {
-        for (int tok = tok0; tok < T; tok += kDecodeWarps / twarps) {
-            const uint4* xrow = reinterpret_cast<const uint4*>(p.x + (int64_t)tok * p.H);
-            float a = 0.0f;
-            for (int c = tpart * 32 + lane; c < p.H / 8; c += twarps * 32) a = fmaxf(a, amax8(__ldg(xrow + c)));
-            a = warp_max(a);
-            if (lane == 0) atomicMax(&S.amax[tok], __float_as_uint(a));
-        }
-    }
-
     const float* logits = p.logits;
-    if (p.wr) {   // logits of experts 2 c and 2 c + 1, then of those 2 G further: four warps an expert
+    if (p.wr) {   // the logits of experts c, c + G, ..: all warps an expert
         logits = p.ws_logits;
-        const int half = warp >> 2, part = warp & 3, HC = p.H / 8;
-        for (int e0 = 2 * cta; e0 < p.E; e0 += 2 * G) {
-            const int e = e0 + half;
-            float acc[8 * NT];
+        const int HC = p.H / 8;
+        for (int e = cta; e < p.E; e += G) {
+            const uint4* w4 = reinterpret_cast<const uint4*>(p.wr + (int64_t)e * p.H);
 #pragma unroll
-            for (int j = 0; j < 8 * NT; ++j) acc[j] = 0.0f;
-            if (!producer && e < p.E) {
-                const uint4* w4 = reinterpret_cast<const uint4*>(p.wr + (int64_t)e * p.H);
-                for (int c = part * 32 + lane; c < HC; c += 128) {
+            for (int n = 0; n < 2; ++n) {
+                if (8 * n >= T) break;
+                float acc[8] = {};
+                for (int c = threadIdx.x; c < HC; c += kDecodeThreads) {
                     float wf[8];
-                    bf16x8_to_f32(__ldg(w4 + c), wf);
+                    const uint4 wv = __ldg(w4 + c);
+                    uint4 xv[8];
 #pragma unroll
-                    for (int j = 0; j < 8 * NT; ++j) {
-                        if (j < T) {
-                            float xf[8];
-                            bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(p.x) + (int64_t)j * HC + c), xf);
+                    for (int j = 0; j < 8; ++j)
+                        xv[j] = 8 * n + j < T ? __ldg(reinterpret_cast<const uint4*>(p.x) + (int64_t)(8 * n + j) * HC + c) : make_uint4(0u, 0u, 0u, 0u);
+                    bf16x8_to_f32(wv, wf);
 #pragma unroll
-                            for (int q = 0; q < 8; ++q) acc[j] = fmaf(xf[q], wf[q], acc[j]);
-                        }
+                    for (int j = 0; j < 8; ++j) {
+                        float xf[8];
+                        bf16x8_to_f32(xv[j], xf);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) acc[j] = fmaf(xf[i], wf[i], acc[j]);
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < 8 * NT; ++j) {
+                for (int j = 0; j < 8; ++j) {
+                    if (8 * n + j >= T) break;
                     const float s = warp_sum(acc[j]);
-                    if (lane == 0) red[warp * 8 * NT + j] = s;
+                    if (lane == 0) S.red[(8 * n + j) * (kDecodeWarps + kDecodeStreams) + warp] = s;
                 }
             }
             __syncthreads();
-            if (threadIdx.x < 2 * T) {
-                const int hh = threadIdx.x / T, j = threadIdx.x % T;
-                if (e0 + hh < p.E) {
-                    float s = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) s += red[(hh * 4 + w) * 8 * NT + j];
-                    p.ws_logits[(int64_t)j * p.E + e0 + hh] = s;
-                }
+            if (threadIdx.x < T) {
+                float s = 0.0f;
+                for (int w = 0; w < kDecodeWarps + kDecodeStreams; ++w) s += S.red[threadIdx.x * (kDecodeWarps + kDecodeStreams) + w];
+                p.ws_logits[(int64_t)threadIdx.x * p.E + e] = s;
             }
             __syncthreads();
         }
         cg::this_grid().sync();
     }
 
-    // S2: a warp a token, the streaming warp (which has nothing else to do yet) first
-    for (int tt = kDecodeWarps - warp; tt < T; tt += kDecodeWarps + 1) {
+    // S2: a warp a token; meanwhile max |x| of the tokens by the others (half a warp's 16 chunks are one token's)
+    for (int tt = warp; tt < T; tt += kDecodeWarps + kDecodeStreams) {
         const float* l = logits + (int64_t)tt * p.E;
         int* ids = S.ids + tt * k;
         float* gates = S.gates + tt * k;
@@ -466,13 +735,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
         if (lane < k) atomicOr(&S.bitmap[ids[lane] >> 5], 1u << (ids[lane] & 31));
     }
     __syncthreads();
-    if (threadIdx.x < P) {   // the pair's expert's place among the touched ones
+    if (threadIdx.x < P) {       // the pair's expert's place among the touched ones
         const int e = S.ids[threadIdx.x], tt = threadIdx.x / k;
-        int r = __popc(S.bitmap[e >> 5] & ((1u << (e & 31)) - 1u));
-        for (int i = 0; i < (e >> 5); ++i) r += __popc(S.bitmap[i]);
-        S.expert[r] = e;
-        S.pick[r][tt] = static_cast<int8_t>(threadIdx.x - tt * k);
-        atomicOr(&S.tokens[r], 1u << tt);
+        int rank = __popc(S.bitmap[e >> 5] & ((1u << (e & 31)) - 1u));
+        for (int i = 0; i < (e >> 5); ++i) rank += __popc(S.bitmap[i]);
+        S.expert[rank] = e;
+        atomicOr(&S.tokens[rank], 1u << tt);
+        S.ids[threadIdx.x] = rank;
     }
     if (threadIdx.x == kDecodeThreads - 1) {
         int n = 0;
@@ -480,441 +749,175 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
         S.n_experts = n;
     }
     __syncthreads();
-    const int n_ex = S.n_experts;
+    if (threadIdx.x < P) {
+        const int tt = threadIdx.x / k, rank = S.ids[threadIdx.x], at = __popc(S.tokens[rank] & ((1u << tt) - 1u));
+        S.list[rank][at] = static_cast<uint8_t>(tt);
+        S.pair[rank][at] = static_cast<uint8_t>(threadIdx.x);
+    }
+    if (threadIdx.x < 4) {       // this CTA's even share of each phase's units
+        const int ph = threadIdx.x;
+        const int per = ph == 0 ? p.N / 8 : ph == 1 ? p.Ns / 8 : p.H / 16, n = per * (ph & 1 ? p.n_shared : S.n_experts);
+        S.per_expert[ph] = per;
+        const int first = share(n, cta, G), end = share(n, cta + 1, G);
+        S.first[ph] = first;
+        S.end[ph] = end;
+        if (ph == 0) {           // the tokens of its experts
+            uint32_t m = 0;
+            for (int e = first / per; e * per < end; ++e) m |= S.tokens[e];
+            int c = 0;
+            for (; m; m &= m - 1) S.need[c++] = __ffs(m) - 1;
+            S.n_need = c;
+        }
+    }
+    __syncthreads();
 
-    // ranges of this CTA
-    const int nb = p.N / 8, nbs = p.Ns / 8;
-    const int a0 = share(n_ex * nb, cta, G), a1 = share(n_ex * nb, cta + 1, G);
-    const int s0 = share(p.n_shared * nbs, cta, G), s1 = share(p.n_shared * nbs, cta + 1, G);
-    const int Vr = n_ex * p.rb.chunks, V = Vr + p.n_shared * p.shared_chunks;   // units of a tile
-    const int v0 = share(tiles * V, cta, G), v1 = share(tiles * V, cta + 1, G);
-    const int row_scale_a = kMx ? p.H / 32 : p.H / 64, row_scale_b = kMx ? p.N / 32 : p.N / 64;   // bytes
-
-    if (producer) {
-        // ---- the weight stream ----
-        DecodeRing r;
-        // One stage: waits for its slot, announces `bytes` and lets each lane issue copies.
-        auto begin = [&](uint32_t bytes) {
-            if (!ws::wait(&S.empty[r.slot], r.phase ^ 1u, &S.abort)) return false;
-            if (lane == 0) tc::mbar_arrive_expect_tx(&S.full[r.slot], bytes);
-            __syncwarp();
-            return true;
-        };
-        // `1 << log` pieces of `rows` rows from piece `z` on, at dst.
-        auto box = [&](int m, uint32_t dst, int rows, int row, int z, int log) {
-            if (!((p.flat >> m) & 1)) {
-                tma_load_3d(dst, &p.map[m], 0, row, z, &S.full[r.slot]);
-            } else {
-                for (int i = 0; i < (1 << log); ++i)
-                    tma_load_2d_at(dst + i * rows * 128, &p.map[m], (z + i) * 128, row, &S.full[r.slot]);
-            }
-        };
-        bool ok = true;
-        for (int pass = 0; pass < 2; ++pass) {   // phase A: routed units, then the shared experts'
-            const DecodeRows& R = pass ? p.rs : p.ra;
-            const int u0 = pass ? s0 : a0, u1 = pass ? s1 : a1, per = pass ? nbs : nb, rows = pass ? p.Ns : p.N;
-            const int upu = kDecodeWarps >> R.wlog;
-            for (int u = u0; ok && u < u1; u += upu) {
-                const int n = min(upu, u1 - u);
-                for (int c = 0; ok && c < R.chunks; ++c) {
-                    const uint32_t unit = 2048u << R.log, sc = pass ? 0u : 16u * row_scale_a;
-                    if (!(ok = begin(n * (unit + sc)))) break;
-                    const uint32_t base = ring + r.slot * p.slot_bytes;
-                    for (int i = lane; i < 4 * n; i += 32) {
-                        const int q = i >> 2, what = i & 3, ei = (u + q) / per, b = (u + q) % per;
-                        const int row = (pass ? ei : S.expert[ei]) * rows + b * 8;
-                        if (what < 2)
-                            box((pass ? 3 : 0) + what, base + q * unit + what * (unit / 2), 8, row, c * 16, R.log);
-                        else if (!pass)
-                            bulk_load(base + kDecodeStage + q * sc + (what - 2) * (sc / 2),
-                                      p.scale[what - 2] + (int64_t)row * row_scale_a, sc / 2, &S.full[r.slot]);
-                    }
-                    __syncwarp();
-                    r.next(p.slots);
-                }
-            }
-        }
-        // phase B: as many stages as there are slots before the barriers, the rest after them
-        int issued = 0, synced = 0;
-        const int upu = kDecodeWarps >> p.rb.wlog;
-        for (int v = v0; ok && v < v1;) {
-            const int tile = v / V, lo = v - tile * V, hi = min(V, lo + v1 - v);
-            for (int q = lo; ok && q < hi; q += upu) {
-                if (issued == p.slots && !synced) {
-                    cg::this_grid().sync();
-                    cg::this_grid().sync();
-                    synced = 1;
-                }
-                const int n = min(upu, hi - q), nr = max(0, min(n, Vr - q));   // routed units among them
-                const uint32_t unit = 2048u << p.rb.log, sc = 16u * row_scale_b;
-                if (!(ok = begin(n * unit + nr * sc))) break;
-                const uint32_t base = ring + r.slot * p.slot_bytes;
-                for (int i = lane; i < 2 * n; i += 32) {
-                    const int j = i >> 1, what = i & 1, id = q + j;
-                    const bool routed = id < Vr;
-                    const int per = routed ? p.rb.chunks : p.shared_chunks, o = routed ? id : id - Vr;
-                    const int row = (routed ? S.expert[o / per] : o / per) * p.H + tile * 16;
-                    if (!what)
-                        box(routed ? 2 : 5, base + j * unit, 16, row, (o % per) << p.rb.log, p.rb.log);
-                    else if (routed)
-                        bulk_load(base + kDecodeStage + j * sc, p.scale[2] + (int64_t)row * row_scale_b, sc, &S.full[r.slot]);
-                }
-                __syncwarp();
-                r.next(p.slots);
-                ++issued;
-            }
-            v += hi - lo;
-        }
-        if (!synced) {
-            cg::this_grid().sync();
-            cg::this_grid().sync();
-        }
-        if (!ok) give_up();
+    if (warp >= kDecodeWarps) {
+        const int to = lane * kDecodeStreams + warp - kDecodeWarps;
+        DecodeStream<kMx> P{p, S, to, smem0 + ring + to * p.slots * p.slot_bytes, smem0 + scales + to * p.slots * p.scale_bytes};
+        if (to < kDecodeWarps) P.enter(0);
+        else P.ph = 4;
+        P.run(true);
+        cg::this_grid().sync();
+        cg::this_grid().sync();
+        P.run(false);
+        cg::this_grid().sync();
+        if (__any_sync(0xffffffffu, !P.ok)) give_up();
         return;
     }
-
-    // ---- the consumer warps ----
-    // S1: the tokens' FP8 codes as B fragments
-    for (int tok = tok0; tok < T; tok += kDecodeWarps / twarps) {
-        const uint4* xrow = reinterpret_cast<const uint4*>(p.x + (int64_t)tok * p.H);
-        const float s = __fdiv_rn(__uint_as_float(S.amax[tok]), kFp8Max);
-        for (int c = tpart * 32 + lane; c < p.H / 8; c += twarps * 32) {
-            const uint2 q = frag_order<kMx>(quant8(__ldg(xrow + c), s));
-            int piece, i, tt, odd;
-            frag_place<kMx>(c, piece, i, tt, odd);
-            const uint32_t at = frags + ((piece * NT + (tok >> 3)) * 4 + i) * 512 + ((tok & 7) * 4 + tt) * 16 + odd * 8;
-            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(q.x), "r"(q.y) : "memory");
+    DecodeWarp<kMx, kF8, kScaleSmem> W{p, S, warp, lane, lane >> 2, lane & 3, lane_row(lane >> 2), ring + warp * p.slots * p.slot_bytes,
+                                       scales + warp * p.slots * p.scale_bytes, frags, xsum};
+    // S1 of the tokens that this CTA's experts have: their FP8 codes as B fragments (half a warp's 16 chunks of
+    // eight columns are one token's)
+    const int xc = p.H / 8, n_x = S.n_need * xc;
+    for (int b0 = warp * 32; b0 < n_x; b0 += 8 * kMul) {
+        const int c0 = b0 + lane;
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = c0 + i * kMul, o = c / xc;
+            v[i] = c < n_x ? __ldg(reinterpret_cast<const uint4*>(p.x) + S.need[o] * xc + c - o * xc) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = c0 + i * kMul;
+            float a = amax8(v[i]);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            if (c < n_x && (lane & 15) == 0) atomicMax(&S.amax[S.need[c / xc]], __float_as_uint(a));
         }
     }
-    consumers_sync();
-
-    DecodeRing r;
-    bool ok = true;
-    auto wait_full = [&]() { ok = ok && ws::wait(&S.full[r.slot], r.phase, &S.abort); };
-    auto release = [&]() {
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&S.empty[r.slot]);
-        r.next(p.slots);
-    };
-    // This warp's sums into set `s` of `red` (one float a lane and register: no bank conflicts).
-    auto put_sums = [&](int s, const float (&acc)[NT][4]) {
+    multipliers_sync();
+    if (threadIdx.x < T) S.sx[threadIdx.x] = __fdiv_rn(__uint_as_float(S.amax[threadIdx.x]), kFp8Max) * kDecodeLadder<kMx>;
+    for (int b0 = warp * 32; b0 < n_x; b0 += 4 * kMul) {
+        const int c0 = b0 + lane;
+        uint4 v[4];
+        int tok[4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) red[((s * kDecodeWarps + warp) * NT * 4 + n * 4 + i) * 32 + lane] = acc[n][i];
-    };
-    // The gate and up sums of output s (unit, token column, row g) of a set of stages.
-    auto get_sums = [&](int s, int wlog, int& unit, int& col, float& gate, float& up) {
-        const int c1 = (s >> 5) & 1, n = (s >> 6) % NT, per = 1 << wlog;
-        unit = s / (64 * NT);
-        col = n * 8 + t * 2 + c1;
-        gate = up = 0.0f;
-        const float* f = red + ((unit << wlog) * NT * 4 + n * 4 + c1) * 32 + lane;
-        for (int w = 0; w < per; ++w) {
-            gate += f[w * NT * 128];
-            up += f[w * NT * 128 + 64];
+        for (int i = 0; i < 4; ++i) {
+            const int c = c0 + i * kMul, o = c / xc;
+            tok[i] = c < n_x ? S.need[o] : -1;
+            v[i] = c < n_x ? __ldg(reinterpret_cast<const uint4*>(p.x) + tok[i] * xc + c - o * xc) : make_uint4(0u, 0u, 0u, 0u);
         }
-    };
-    const int batch = p.batch;
-
-    // phase A, routed units: h = silu(G) U.  A batch of stages, then their sums over the warps.
-    {
-        const int upu = kDecodeWarps >> p.ra.wlog, slot_unit = warp >> p.ra.wlog;
-        const int pair0 = warp & ((1 << p.ra.wlog) - 1);          // which two pieces of a chunk
-        const uint32_t row_off = slot_unit * (2048 << p.ra.log) + 2 * pair0 * 1024 + g * 128, row_b = 1024 << p.ra.log;
-        const uint32_t sc_off = kDecodeStage + (slot_unit * 16 + g) * row_scale_a;
-        uint32_t f[64];
-        float2 off[4];
-        int held = -1;   // what f holds: two pieces of one block of tokens
-        int ei = a0 / nb, left = nb - a0 % nb;   // the expert of unit u and how many of its units are left
-        for (int u = a0; u < a1; u += upu * batch) {
-#pragma unroll 1
-            for (int s = 0; s < batch && u + s * upu < a1; ++s) {
-                int e = ei;                      // this warp's expert
-                for (int ahead = s * upu + slot_unit - left; ahead >= 0; ahead -= nb) ++e;
-                const bool mine = u + s * upu + slot_unit < a1;
-                const uint32_t toks = NT > 1 && mine ? S.tokens[e] : 0xFFu;
-                float acc[NT][4] = {};
-                for (int c = 0; c < p.ra.chunks; ++c) {
-                    const int pair = c * 8 + pair0, halves = p.H / 128 - 4 * pair;
-                    wait_full();
-                    if (ok && mine && halves > 0) {
-                        const uint32_t base = ring + r.slot * p.slot_bytes;
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            if (NT > 1 && !((toks >> (8 * n)) & 0xFFu)) continue;
-                            if (held != pair * NT + n) {
-                                held = pair * NT + n;
-                                uint4 q[8];
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    q[i] = i < 2 * halves ? lds128(frags + (((2 * pair + (i >> 2)) * NT + n) * 4 + (i & 3)) * 512 + lane * 16)
-                                                          : make_uint4(0u, 0u, 0u, 0u);
-                                frags_f16<kMx>(q, f);
-                                if constexpr (!kMx) nibble_offsets(f, off);
-                            }
-                            pieces_mma<kMx>(base + row_off, base + row_off + row_b, 1024, base + sc_off + pair * (kMx ? 16 : 8),
-                                            base + sc_off + 8 * row_scale_a + pair * (kMx ? 16 : 8), halves, f, off, acc[n]);
-                        }
-                    }
-                    release();
-                }
-                put_sums(s, acc);
+        for (int u = 0; u < 4; ++u) {
+            const int c = c0 + u * kMul, tk = tok[u], c8 = c % xc;
+            const bool live = tk >= 0;
+            const RowQuant s = RowQuant::of(live ? __uint_as_float(S.amax[tk]) : 0.0f);
+            float x[8];
+            bf16x8_to_f32(v[u], x);
+            const uint2 codes = s.codes(x);
+            int piece, i, tt;
+            frag_place<kMx>(c8, piece, i, tt);
+            if (live) {
+                if constexpr (kF8)
+                    *reinterpret_cast<uint2*>(g_decode_smem + frags + (tk * pieces_x + piece) * 256 + (((i >> 1) ^ (tk & 3)) * 64) + tt * 16 + (i & 1) * 8) =
+                        frag_order<kMx>(codes);
+                else
+                    *reinterpret_cast<uint4*>(g_decode_smem + frags + (tk * pieces_x + piece) * 512 + ((i ^ (tk & 7)) * 64) + tt * 16) =
+                        frag_f16<kMx>(frag_order<kMx>(codes));
             }
-            consumers_sync();
-            const int n_out = min(batch * upu, a1 - u) * 64 * NT;
-            for (int s = threadIdx.x; s < n_out; s += 32 * kDecodeWarps) {
-                int unit, col;
-                float gt, up;
-                get_sums(s, p.ra.wlog, unit, col, gt, up);
-                int e = ei, b = unit + nb - left;
-                for (; b >= nb; b -= nb) ++e;
-                if (col >= T || !((S.tokens[e] >> col) & 1u)) continue;
-                const float sx = __fdiv_rn(__uint_as_float(S.amax[col]), kFp8Max) * kDecodeLadder<kMx>;
-                p.h[(int64_t)(col * k + S.pick[e][col]) * p.N + b * 8 + g] = silu(gt * sx) * (up * sx);
+            if constexpr (!kMx) {
+                const float sum = halfwarp_sum(e4m3x8_sum(codes));
+                if (live && (lane & 15) == 0)
+                    *reinterpret_cast<float*>(g_decode_smem + xsum + (tk * pieces_x * 2 + (c8 >> 4)) * 4) = sum * kNibbleOffset;
             }
-            consumers_sync();
-            for (left -= upu * batch; left <= 0; left += nb) ++ei;
         }
     }
-    // phase A, shared experts: the same on bf16 weights and tokens
-    {
-        const int upu = kDecodeWarps >> p.rs.wlog, slot_unit = warp >> p.rs.wlog;
-        const int pair0 = warp & ((1 << p.rs.wlog) - 1);
-        const uint32_t row_off = slot_unit * (2048 << p.rs.log) + 2 * pair0 * 1024 + g * 128, row_b = 1024 << p.rs.log;
-        for (int u = s0; u < s1; u += upu) {
-            float acc[NT][4] = {};
-            for (int c = 0; c < p.rs.chunks; ++c) {
-                const int piece = 2 * (c * 8 + pair0);
-                const bool mine = u + slot_unit < s1 && piece < p.rs.pieces;   // pieces: even, 2 H bytes
-                uint4 b[NT][2][2] = {};
-                if (mine) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (n * 8 + g < T)
-                                b[n][i >> 1][i & 1] = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)(n * 8 + g) * p.H) + piece * 8 + i * 4 + t);
-                }
-                wait_full();
-                if (ok && mine) {
-                    const uint32_t row = ring + r.slot * p.slot_bytes + row_off;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int pc = 0; pc < 2; ++pc) piece_mma_bf16(row + pc * 1024, row + row_b + pc * 1024, b[n][pc], acc[n]);
-                }
-                release();
-            }
-            put_sums(0, acc);
-            consumers_sync();
-            const int n_out = min(upu, s1 - u) * 64 * NT;
-            for (int s = threadIdx.x; s < n_out; s += 32 * kDecodeWarps) {
-                int unit, col;
-                float gt, up;
-                get_sums(s, p.rs.wlog, unit, col, gt, up);
-                if (col >= T) continue;
-                const float a = silu(gt) * up;
-                const uint16_t hi = f32_to_bf16_bits(a);   // hi + lo: 16 bits of the activation
-                const int64_t at = (int64_t)col * p.n_shared * p.Ns + (u + unit) * 8 + g;
-                p.act_hi[at] = hi;
-                p.act_lo[at] = f32_to_bf16_bits(a - bf16_bits_to_f32(hi));
-            }
-            consumers_sync();
-        }
-    }
+    multipliers_sync();
+
+    W.template routed<false>();
+    if (p.n_shared) W.template shared<false>();
 
     cg::this_grid().sync();
-    // S5: pair q's codes as B fragments, by CTA q
-    const int hq_row = ((p.N + 255) / 256) * 256;
-    for (int q = cta; q < P; q += G) {
-        const float4* src = reinterpret_cast<const float4*>(p.h + (int64_t)q * p.N);
+    // S5: pair r's codes as B fragments, by CTA r
+    for (int r = cta; r < P; r += G) {
+        const float4* src = reinterpret_cast<const float4*>(p.h + (int64_t)r * p.N);
         float a = 0.0f;
-        for (int c = threadIdx.x; c < p.N / 4; c += 32 * kDecodeWarps) {
+        for (int c = threadIdx.x; c < p.N / 4; c += kMul) {
             const float4 v = __ldcg(src + c);
             a = fmaxf(fmaxf(a, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
         }
         a = warp_max(a);
-        consumers_sync();
         if (lane == 0) S.red[warp] = a;
-        consumers_sync();
-        a = warp_max(S.red[lane & (kDecodeWarps - 1)]);
-        const float s = __fdiv_rn(a, kFp8Max);
-        for (int c = threadIdx.x; c < p.N / 8; c += 32 * kDecodeWarps) {   // whole half-warps: N is a multiple of 128
-            uint2 codes = make_uint2(0u, 0u);
-            if (s != 0.0f) {
+        multipliers_sync();
+        const RowQuant s = RowQuant::of(warp_max(lane < kDecodeWarps ? S.red[lane] : 0.0f));
+        for (int c0 = warp * 32; c0 < p.N / 8; c0 += kMul) {
+            const int c = c0 + lane;
+            const bool live = c < p.N / 8;
+            float x[8] = {};
+            if (live) {
                 const float4 v = __ldcg(src + 2 * c), w = __ldcg(src + 2 * c + 1);
-                codes.x = static_cast<uint32_t>(f32x2_to_e4m3x2(__fdiv_rn(v.x, s), __fdiv_rn(v.y, s))) |
-                          (static_cast<uint32_t>(f32x2_to_e4m3x2(__fdiv_rn(v.z, s), __fdiv_rn(v.w, s))) << 16);
-                codes.y = static_cast<uint32_t>(f32x2_to_e4m3x2(__fdiv_rn(w.x, s), __fdiv_rn(w.y, s))) |
-                          (static_cast<uint32_t>(f32x2_to_e4m3x2(__fdiv_rn(w.z, s), __fdiv_rn(w.w, s))) << 16);
+                x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+                x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
             }
-            int piece, i, tt, odd;
-            frag_place<kMx>(c, piece, i, tt, odd);
-            *reinterpret_cast<uint2*>(p.hq + (int64_t)q * hq_row + piece * 256 + i * 64 + tt * 16 + odd * 8) =
-                frag_order<kMx>(codes);
-            if constexpr (!kMx) {   // the sums of the 128-column groups, for the nibbles' offset
-                float sum = e4m3x8_sum(codes);
-                const uint32_t half = 0xFFFFu << (lane & 16);
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(half, sum, o);
-                if ((c & 15) == 0) p.hsum[(int64_t)q * (hq_row / 128) + (c >> 4)] = sum * kNibbleOffset;
+            const uint2 codes = s.codes(x);
+            int piece, i, tt;
+            frag_place<kMx>(c, piece, i, tt);
+            if (live)
+                *reinterpret_cast<uint4*>(p.hq + ((int64_t)r * pieces_h + piece) * 512 + i * 64 + tt * 16) = frag_f16<kMx>(frag_order<kMx>(codes));
+            if constexpr (!kMx) {
+                const float sum = halfwarp_sum(e4m3x8_sum(codes));
+                if (live && (lane & 15) == 0) p.hsum[(int64_t)r * pieces_h * 2 + (c >> 4)] = sum * kNibbleOffset;
             }
         }
-        if (threadIdx.x == 0) p.gs[q] = S.gates[q] * s * kDecodeLadder<kMx>;
+        if (threadIdx.x == 0) p.gs[r] = S.gates[r] * s.s * kDecodeLadder<kMx>;
+        multipliers_sync();
     }
     cg::this_grid().sync();
     if (threadIdx.x < P) S.gs[threadIdx.x] = __ldcg(p.gs + threadIdx.x);
-    consumers_sync();
+    multipliers_sync();
 
-    // phase B.  The FP8 activations of a warp's next stage (its first block of tokens) are fetched
-    // while it works on this one.
-    const int upu = kDecodeWarps >> p.rb.wlog, slot_unit = warp >> p.rb.wlog;
-    const int pair0 = warp & ((1 << p.rb.wlog) - 1), pairs = 1 << p.rb.wlog;   // of a unit
-    const uint32_t row_off = slot_unit * (2048 << p.rb.log) + 2 * pair0 * 2048 + g * 128;
-    const uint32_t sc_off = kDecodeStage + (slot_unit * 16 + g) * row_scale_b;
-    uint4 q[8] = {};
-    float2 off[4] = {};
-    // Block n of routed expert ei's activations at columns 512 pair ..
-    auto fetch = [&](int ei, int pair, int n) {
-        const int halves = p.N / 128 - 4 * pair, col = n * 8 + g;
-        const uint32_t toks = S.tokens[ei];
-        const bool on = (toks >> col) & 1u;
-        const uint4* src = reinterpret_cast<const uint4*>(p.hq + (int64_t)(on ? col * k + S.pick[ei][col] : 0) * hq_row + pair * 512) + t;
+    W.template routed<true>();
+    if (p.n_shared) W.template shared<true>();
+
+    cg::this_grid().sync();
+    // S7: the gated rows in selection order, then the shared experts
+    for (int i = cta * kMul + threadIdx.x; i < T * p.H / 4; i += G * kMul) {
+        const int tt = i / (p.H / 4), m4 = i - tt * (p.H / 4);
+        float4 v[kMaxK];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = on && i < 2 * halves ? __ldcg(src + (i >> 2) * 16 + (i & 3) * 4) : make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (!kMx) {
-            float f[2][4] = {};
+        for (int j = 0; j < kMaxK; ++j)
+            if (j < k) v[j] = __ldcg(reinterpret_cast<const float4*>(p.y + (int64_t)(tt * k + j) * p.H) + m4);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int c1 = 0; c1 < 2; ++c1) {
-                const int c2 = n * 8 + t * 2 + c1;
-                if ((toks >> c2) & 1u) {
-                    const float* hs = p.hsum + (int64_t)(c2 * k + S.pick[ei][c2]) * (hq_row / 128) + 4 * pair;
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) f[c1][h] = h < halves ? __ldcg(hs + h) : 0.0f;
-                }
-            }
-#pragma unroll
-            for (int h = 0; h < 4; ++h) off[h] = make_float2(f[0][h], f[1][h]);
+        for (int j = 0; j < kMaxK; ++j)
+            if (j < k) { o.x += v[j].x; o.y += v[j].y; o.z += v[j].z; o.w += v[j].w; }
+        for (int s = 0; s < p.n_shared; ++s) {
+            const float4 w = __ldcg(reinterpret_cast<const float4*>(p.y + (int64_t)(P + s * T + tt) * p.H) + m4);
+            o.x += w.x; o.y += w.y; o.z += w.z; o.w += w.w;
         }
-    };
-    auto first_block = [&](int ei) { return NT > 1 && !(S.tokens[ei] & 0xFFu) ? 1 : 0; };
-    // The next stage's first block, where the warp's unit there is a routed expert's.
-    auto prefetch = [&](int id, int hi) {
-        if (id < hi && id < Vr) fetch(id / p.rb.chunks, (id % p.rb.chunks) * pairs + pair0, first_block(id / p.rb.chunks));
-    };
-    for (int v = v0; v < v1;) {
-        const int tile = v / V, lo = v - tile * V, hi = min(V, lo + v1 - v);
-        float acc[NT][4] = {};
-        prefetch(lo + slot_unit, hi);
-        for (int u = lo; u < hi; u += upu) {
-            const int id = u + slot_unit;
-            const uint32_t base = ring + r.slot * p.slot_bytes;
-            if (id < Vr && id < hi) {
-                const int ei = id / p.rb.chunks, pair = (id % p.rb.chunks) * pairs + pair0, halves = p.N / 128 - 4 * pair;
-                const uint32_t toks = S.tokens[ei];
-                uint32_t f[64];
-                float2 o[4];
-                frags_f16<kMx>(q, f);
-#pragma unroll
-                for (int h = 0; h < 4; ++h) o[h] = off[h];
-                prefetch(id + upu, hi);
-                wait_full();
-                if (ok && halves > 0) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if (NT > 1 && !((toks >> (8 * n)) & 0xFFu)) continue;
-                        if (NT > 1 && n != first_block(ei)) {      // a second block: fetched now, the next stage's again after it
-                            fetch(ei, pair, n);
-                            frags_f16<kMx>(q, f);
-#pragma unroll
-                            for (int h = 0; h < 4; ++h) o[h] = off[h];
-                            prefetch(id + upu, hi);
-                        }
-                        float y[4] = {};
-                        pieces_mma<kMx>(base + row_off, base + row_off + 1024, 2048, base + sc_off + pair * (kMx ? 16 : 8),
-                                        base + sc_off + 8 * row_scale_b + pair * (kMx ? 16 : 8), halves, f, o, y);
-#pragma unroll
-                        for (int c1 = 0; c1 < 2; ++c1) {
-                            const int col = n * 8 + t * 2 + c1;
-                            if ((toks >> col) & 1u) {   // the other columns hold nothing of this expert's
-                                const float fac = S.gs[col * k + S.pick[ei][col]];
-                                acc[n][c1] = fmaf(fac, y[c1], acc[n][c1]);
-                                acc[n][c1 + 2] = fmaf(fac, y[c1 + 2], acc[n][c1 + 2]);
-                            }
-                        }
-                    }
-                }
-            } else {
-                const int o = id - Vr, e = o / max(1, p.shared_chunks), piece = ((o % max(1, p.shared_chunks)) << p.rb.log) + 2 * pair0;
-                const bool mine = id < hi && piece < p.Ns / 64;
-                uint4 b[NT][2][2][2] = {};   // hi and lo
-                if (mine) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (n * 8 + g < T && (i < 2 || p.rb.log > 0)) {
-                                const int64_t at = ((int64_t)(n * 8 + g) * p.n_shared + e) * (p.Ns / 8) + piece * 8 + i * 4 + t;
-                                b[n][0][i >> 1][i & 1] = __ldcg(reinterpret_cast<const uint4*>(p.act_hi) + at);
-                                b[n][1][i >> 1][i & 1] = __ldcg(reinterpret_cast<const uint4*>(p.act_lo) + at);
-                            }
-                }
-                wait_full();
-                if (ok && mine) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int pc = 0; pc < 2; ++pc) {
-                            if (pc && p.rb.log == 0) break;   // the unit has one piece
-#pragma unroll
-                            for (int part = 0; part < 2; ++part)
-                                piece_mma_bf16(base + row_off + pc * 2048, base + row_off + 1024 + pc * 2048, b[n][part][pc], acc[n]);
-                        }
-                }
-            }
-            release();
-        }
-        put_sums(0, acc);
-        consumers_sync();
-        const bool whole = hi - lo == V;
-        float* part = p.part + (int64_t)(tile + cta) * (128 * NT);   // tile + cta: its own for each (tile, CTA)
-        float sum = 0.0f;
-        const int s = threadIdx.x;
-        if (s < 128 * NT)
-            for (int w = 0; w < kDecodeWarps; ++w) sum += red[w * NT * 128 + s];
-        if (!whole) {
-            if (s < 128 * NT) part[s] = sum;
-            __threadfence();
-            consumers_sync();
-            // the CTAs that hold a piece of this tile: first .. last (those with an empty share hold none)
-            const int U = tiles * V, f0 = tile * V, f1 = f0 + V - 1;
-            const int first = static_cast<int>(((int64_t)(f0 + 1) * G - 1) / U), last = static_cast<int>(((int64_t)(f1 + 1) * G - 1) / U);
-            const int parts = U >= G ? last - first + 1 : V;
-            if (threadIdx.x == 0) S.last = atomicAdd(p.count + tile, 1u) == (unsigned)(parts - 1);
-            consumers_sync();
-            if (S.last) {
-                __threadfence();
-                sum = 0.0f;
-                if (s < 128 * NT)
-                    for (int c = first; c <= last; ++c)
-                        if (share(U, c, G) < share(U, c + 1, G)) sum += __ldcg(p.part + (int64_t)(tile + c) * (128 * NT) + s);
-            }
-        }
-        if (s < 128 * NT && (whole || S.last)) {
-            const int i = s >> 5, col = (i >> 2) * 8 + t * 2 + (i & 1), m = tile * 16 + g + 8 * ((i >> 1) & 1);
-            if (col < T) p.out[(int64_t)col * p.H + m] = f32_to_bf16_bits(sum);
-        }
-        consumers_sync();   // red is free for the next tile
-        v += hi - lo;
+        uint2 packed;
+        packed.x = static_cast<uint32_t>(f32_to_bf16_bits(o.x)) | (static_cast<uint32_t>(f32_to_bf16_bits(o.y)) << 16);
+        packed.y = static_cast<uint32_t>(f32_to_bf16_bits(o.z)) | (static_cast<uint32_t>(f32_to_bf16_bits(o.w)) << 16);
+        reinterpret_cast<uint2*>(p.out + (int64_t)tt * p.H)[m4] = packed;
     }
-    if (!ok) give_up();
+    if (!W.ok) give_up();
 }
 
 // ---- host ---------------------------------------------------------------------------------------
 
 struct DecodePlan {
-    size_t logits, h, hq, gs, hsum, act, part, count, total;
+    size_t logits, h, hq, hsum, gs, act, y, total;
 };
 
 inline DecodePlan plan_decode(const DecodeLayer& L, int64_t T, int k) {
@@ -925,15 +928,14 @@ inline DecodePlan plan_decode(const DecodeLayer& L, int64_t T, int k) {
         off = align_up(off + (bytes ? bytes : 1), 256);
         return at;
     };
-    const size_t P = (size_t)T * k, nt = (T + 7) / 8;
+    const size_t P = (size_t)T * k;
     p.logits = take((size_t)T * L.E * 4);
     p.h = take(P * L.N * 4);
-    p.hq = take(P * align_up(L.N, 256));
-    p.gs = take(P * 4);
+    p.hq = take(P * align_up(L.N, 256) * 2);                   // f16 values
     p.hsum = take(P * (align_up(L.N, 256) / 128) * 4);
+    p.gs = take(P * 4);
     p.act = take((size_t)T * L.n_shared * L.shared_N * 4);     // hi, then lo
-    p.part = take((size_t)(L.H / 16 + kDecodeMaxGrid) * 128 * nt * 4);
-    p.count = take((size_t)(L.H / 16) * 4);
+    p.y = take((P + (size_t)T * L.n_shared) * L.H * 4);        // routed rows, then the shared experts'
     p.total = off;
     return p;
 }
@@ -949,49 +951,63 @@ inline int decode_args_ok(const DecodeLayer& L, int64_t T, int k) {
     return MOE_OK;
 }
 
-inline DecodeRows decode_rows(int64_t row_bytes, int log = -1) {
+inline DecodeRows decode_rows(int64_t row_bytes, int cp) {
     DecodeRows r{};
     r.pieces = static_cast<int>((row_bytes + 127) / 128);
-    while (r.log < 4 && (1 << r.log) < r.pieces) ++r.log;
-    if (log >= 0) r.log = log;
-    r.wlog = r.log > 0 ? r.log - 1 : 0;
-    r.chunks = (r.pieces + (1 << r.log) - 1) >> r.log;
+    r.cp = std::min(cp, r.pieces);
+    r.chunks = (r.pieces + r.cp - 1) / r.cp;
     return r;
 }
 
 // Weight rows as [piece][row][128 bytes]: a 3-D view where rows are whole pieces, else a 2-D one.
-inline bool decode_map(CUtensorMap* m, const void* w, uint64_t row_bytes, uint64_t rows, uint32_t box_rows, int log, bool* flat) {
+inline bool decode_map(CUtensorMap* m, const void* w, uint64_t row_bytes, uint64_t rows, uint32_t box_rows, int cp, bool* flat) {
     *flat = row_bytes % 128 != 0;
     if (*flat) return make_map_u8(m, w, row_bytes, rows, 128, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
     const cuuint64_t dims[3] = {128, rows, row_bytes / 128};
     const cuuint64_t strides[2] = {row_bytes, 128};
-    const cuuint32_t box[3] = {128, box_rows, 1u << log};
+    const cuuint32_t box[3] = {128, box_rows, static_cast<cuuint32_t>(cp)};
     return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, w, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <bool kMx, int NT>
-inline int launch_decode(DecodeParams& q, cudaStream_t stream) {
-    const size_t scale_a = (size_t)(kDecodeWarps >> q.ra.wlog) * 16 * (kMx ? q.H / 32 : q.H / 64);
-    const size_t scale_b = (size_t)(kDecodeWarps >> q.rb.wlog) * 16 * (kMx ? q.N / 32 : q.N / 64);
-    q.slot_bytes = static_cast<int>(align_up(kDecodeStage + std::max(scale_a, scale_b), 1024));
-    const size_t frag = (size_t)((q.H + 255) / 256) * NT * kDecodePiece;
-    const size_t room = 227 * 1024 - sizeof(DecodeShared) - 1024 - 256 - frag;   // of a CTA's 227 KB
-    size_t red = 0;
-    for (q.batch = kDecodeBatch; q.batch > 0; q.batch >>= 1) {   // fewer stages a sum where slots are short
-        red = (size_t)q.batch * kDecodeWarps * NT * 128 * 4;
-        q.slots = static_cast<int>(std::min<size_t>(kDecodeMaxSlots, (room - red) / q.slot_bytes));
-        if (q.slots >= 4 || q.batch == 1) break;
-    }
-    if (q.slots < 2) return MOE_ERR_UNSUPPORTED_SHAPE;
-    const size_t smem = 1024 + (size_t)q.slots * q.slot_bytes + frag + red;
-    const void* fn = reinterpret_cast<const void*>(k_decode<kMx, NT>);
+// How a CTA's 227 KB are divided: the tokens' fragments (f16, or FP8 where they would take more than a third),
+// their group sums, and the warps' rings: chunks of four pieces (8 KB) where two fit, else of two or one.  The
+// rows' scales get buffers beside the slots where they fit, else they are read in place.
+struct DecodeSmem {
+    int cp, slots, scale_bytes;
+    bool f8;
+    size_t bytes;
+};
+
+inline bool plan_decode_smem(const DecodeLayer& L, int64_t T, bool mx, DecodeSmem* out) {
+    const size_t pieces = (L.H + 255) / 256, room = 227 * 1024 - sizeof(DecodeShared) - 1024 - 64;
+    const bool f8 = T * pieces * 512 > 72 * 1024;
+    const size_t scale = align_up((size_t)16 * std::max(L.H, L.N) / (mx ? 32 : 64), 128);
+    for (int in_smem = 1; in_smem >= 0; --in_smem)
+        for (int cp = 4; cp >= 1; cp >>= 1)
+            for (int slots = kDecodeMaxSlots; slots >= 2; --slots) {
+                out->f8 = f8 || !in_smem;
+                const size_t fixed = T * pieces * (out->f8 ? 256 : 512) + (mx ? 0 : T * pieces * 8);
+                const size_t ring = (size_t)kDecodeWarps * slots * (cp * 2048 + (in_smem ? scale : 0));
+                if (fixed + ring > room) continue;
+                out->cp = cp;
+                out->slots = slots;
+                out->scale_bytes = in_smem ? static_cast<int>(scale) : 0;
+                out->bytes = 1024 + fixed + ring;
+                return true;
+            }
+    return false;
+}
+
+template <bool kMx, bool kF8, bool kScaleSmem>
+inline int launch_decode(DecodeParams& q, size_t smem, cudaStream_t stream) {
+    const void* fn = reinterpret_cast<const void*>(k_decode<kMx, kF8, kScaleSmem>);
     if (set_smem(fn, smem)) return MOE_ERR_CUDA;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return MOE_ERR_CUDA;
     void* args[] = {&q};
-    if (cudaLaunchCooperativeKernel(fn, dim3(std::min(sms, kDecodeMaxGrid)), dim3(kDecodeThreads), args, smem, stream) != cudaSuccess) {
+    if (cudaLaunchCooperativeKernel(fn, dim3(sms), dim3(kDecodeThreads), args, smem, stream) != cudaSuccess) {
         (void)cudaGetLastError();   // a rejected launch leaves no error behind for later calls
         return MOE_ERR_CUDA;
     }
@@ -1018,18 +1034,21 @@ inline int decode_impl(const DecodeLayer& L, const uint16_t* x, const float* log
     if (!aligned(ws, 256)) return MOE_ERR_MISALIGNED;
     uint8_t* b = static_cast<uint8_t*>(ws);
     DecodeParams q{};
-    q.ra = decode_rows(L.H / 2);
-    q.rb = decode_rows(L.N / 2);
-    if (L.n_shared > 0) {
-        q.rs = decode_rows((int64_t)L.H * 2);
-        q.shared_chunks = decode_rows((int64_t)L.shared_N * 2, q.rb.log).chunks;
-    }
+    DecodeSmem m;
+    if (!plan_decode_smem(L, T, kMx, &m)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    q.slots = m.slots;
+    q.slot_bytes = m.cp * 2048;
+    q.scale_bytes = m.scale_bytes;
+    q.rows[0] = decode_rows(L.H / 2, m.cp);
+    q.rows[1] = decode_rows((int64_t)L.H * 2, m.cp);
+    q.rows[2] = decode_rows(L.N / 2, m.cp);
+    q.rows[3] = decode_rows((int64_t)(L.n_shared > 0 ? L.shared_N : 128) * 2, m.cp);
     for (int i = 0; i < (L.n_shared > 0 ? 6 : 3); ++i) {
         const bool sh = i >= 3, down = i % 3 == 2;
         const uint64_t cols = down ? (sh ? L.shared_N : L.N) : L.H, rows = down ? L.H : (sh ? L.shared_N : L.N);
         bool flat;
         if (!decode_map(&q.map[i], sh ? static_cast<const void*>(L.sw[i - 3]) : L.w[i], sh ? cols * 2 : cols / 2,
-                        rows * (sh ? L.n_shared : L.E), down ? 16 : 8, down ? q.rb.log : sh ? q.rs.log : q.ra.log, &flat))
+                        rows * (sh ? L.n_shared : L.E), down ? 16 : 8, q.rows[(down ? 2 : 0) + (sh ? 1 : 0)].cp, &flat))
             return MOE_ERR_CUDA;
         q.flat |= flat ? 1 << i : 0;
     }
@@ -1045,12 +1064,13 @@ inline int decode_impl(const DecodeLayer& L, const uint16_t* x, const float* log
     q.hsum = reinterpret_cast<float*>(b + p.hsum);
     q.act_hi = reinterpret_cast<uint16_t*>(b + p.act);
     q.act_lo = q.act_hi + (size_t)T * L.n_shared * L.shared_N;
-    q.part = reinterpret_cast<float*>(b + p.part);
-    q.count = reinterpret_cast<unsigned*>(b + p.count);
+    q.y = reinterpret_cast<float*>(b + p.y);
     q.E = L.E; q.H = L.H; q.N = L.N; q.k = k; q.T = static_cast<int>(T);
     q.n_shared = L.n_shared;
     q.Ns = L.n_shared > 0 ? L.shared_N : 0;
-    return T <= 8 ? launch_decode<kMx, 1>(q, stream) : launch_decode<kMx, 2>(q, stream);
+    return !m.scale_bytes ? launch_decode<kMx, true, false>(q, m.bytes, stream)
+           : m.f8         ? launch_decode<kMx, true, true>(q, m.bytes, stream)
+                          : launch_decode<kMx, false, true>(q, m.bytes, stream);
 }
 
 inline DecodeLayer decode_layer(const moe_w4a8_layer& L) {

@@ -81,6 +81,7 @@ struct alignas(64) DecodeParams {
     DecodeRows rows[4];           // gate/up, shared gate/up, down, shared down
     int E, H, N, k, T, n_shared, Ns;
     int slots, slot_bytes, scale_bytes;   // scale_bytes: of one of a warp's `slots` scale buffers, 0: read in place
+    int frag_bytes, max_rows;     // of the fragments in shared memory; rows of h that fit there
     int flat;                     // bit i set: map i is 2-D (rows are not whole pieces)
 };
 
@@ -158,6 +159,10 @@ __device__ __forceinline__ void frag_place(int c8, int& piece, int& i, int& t) {
     piece = c8 >> 5;
     i = 4 * ((c8 >> 4) & 1) + j;
 }
+
+// Bytes of a row of fragments (64 more than they take: neighbouring rows then start in different banks).
+template <bool kF8>
+__host__ __device__ constexpr uint32_t frag_row_bytes(int pieces) { return pieces * (kF8 ? 256 : 512) + 64; }
 
 constexpr float kNibbleOffset = -8.0f / 16777216.0f;   // -8 2^-24
 // The power of two that the routed products' sums lack.
@@ -298,7 +303,7 @@ constexpr int kMul = 32 * kDecodeWarps;   // threads that multiply
 __device__ __forceinline__ void multipliers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kMul) : "memory"); }
 
 // The first unit of CTA c's even share of n units.
-__device__ __forceinline__ int share(int n, int c, int G) { return static_cast<int>((int64_t)n * c / G); }
+__device__ __forceinline__ int share(int n, int c, int G) { return static_cast<int>((unsigned)n * (unsigned)c / (unsigned)G); }   // n c < 2^32: n <= 2^17, a few hundred CTAs
 
 // S2 of one token by one warp, as topk_row (ranked by logit descending, index ascending; NaN as
 // -inf), with the warp's maximum and the lowest index that has it in two redux instructions: the
@@ -350,18 +355,18 @@ struct RowQuant {
         return q;
     }
     __device__ __forceinline__ float divide(float x) const {
+        if (plain) return __fdiv_rn(x, s);
         const float q = x * r;
         return fmaf(fmaf(-q, s, x), r, q);
     }
     __device__ __forceinline__ uint2 codes(const float (&x)[8]) const {
-        uint2 c = make_uint2(0u, 0u);
-        if (s == 0.0f) return c;
+        uint32_t c[2] = {0u, 0u};
+        if (s != 0.0f) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = plain ? __fdiv_rn(x[2 * i], s) : divide(x[2 * i]), b = plain ? __fdiv_rn(x[2 * i + 1], s) : divide(x[2 * i + 1]);
-            (i < 2 ? c.x : c.y) |= static_cast<uint32_t>(f32x2_to_e4m3x2(a, b)) << (16 * (i & 1));
+            for (int i = 0; i < 4; ++i)
+                c[i >> 1] |= static_cast<uint32_t>(f32x2_to_e4m3x2(divide(x[2 * i]), divide(x[2 * i + 1]))) << (16 * (i & 1));
         }
-        return c;
+        return make_uint2(c[0], c[1]);
     }
 };
 
@@ -383,9 +388,12 @@ struct DecodeShared {
     uint32_t bitmap[kMaxE / 32];
     unsigned amax[kDecodeMaxT];
     float sx[kDecodeMaxT];
-    float red[(kDecodeWarps + kDecodeStreams) * kDecodeMaxT];
+    float red[2 * (kDecodeWarps + kDecodeStreams) * kDecodeMaxT];
     int first[4], end[4], per_expert[4];             // this CTA's units of each phase, and how many an expert has
     int need[kDecodeMaxT], n_need;
+    uint8_t place[kDecodeMaxPairs][kDecodeMaxT];     // of expert place_e + i's pairs among the pairs of this CTA's down rows
+    uint8_t row_pair[kDecodeMaxPairs];               // and those pairs
+    int place_e, n_rows, most_rows;                  // n_rows of them; the most that any CTA has
     int n_experts;
     volatile int abort;
 };
@@ -473,7 +481,7 @@ struct DecodeWarp {
     const DecodeParams& p;
     DecodeShared& S;
     int warp, lane, g, t, r;                        // r: the lane's row
-    uint32_t slots0, scales0, frags, xsum;          // offsets in the dynamic shared memory; slots0, scales0: the warp's
+    uint32_t slots0, scales0, frags, sums;          // offsets in the dynamic shared memory; slots0, scales0: the warp's
     int slot = 0, buf = 0;
     uint32_t parity = 0;
     bool ok = true;
@@ -484,23 +492,26 @@ struct DecodeWarp {
         if (lane == 0) tc::mbar_arrive(&S.empty[warp][slot]);
         if (++slot == p.slots) { slot = 0; parity ^= 1u; }
     }
-    template <bool kDown>
+    // kGlobal: the B fragments come from the workspace, else from shared memory.
+    template <bool kDown, bool kGlobal>
     __device__ __forceinline__ void routed();
     template <bool kDown>
     __device__ __forceinline__ void shared();
 };
 
 template <bool kMx, bool kF8, bool kScaleSmem>
-template <bool kDown>
+template <bool kDown, bool kGlobal>
 __device__ __forceinline__ void DecodeWarp<kMx, kF8, kScaleSmem>::routed() {
     constexpr int ph = kDown ? 2 : 0;
     const DecodeRows R = p.rows[ph];
     const int K = kDown ? p.N : p.H, pieces = (K + 255) / 256, per = S.per_expert[ph], end = S.end[ph];
     const uint32_t rs = kMx ? K / 32 : K / 64, step = kDown ? 2048 : 1024, row_b = kDown ? 1024u : 1024u * R.cp;
-    const uint32_t frag_row = pieces * (kF8 && !kDown ? 256 : 512);
+    const uint32_t frag_row = frag_row_bytes<kF8 && !kDown>(pieces);
     for (int u = S.first[ph] + warp; u < end; u += kDecodeWarps) {
         const int e = u / per, b = u - e * per, n_tok = __popc(S.tokens[e]);
-        const uint8_t* of = kDown ? S.pair[e] : S.list[e];   // the columns' pairs (tokens)
+        // where the columns' fragments are: by pair in the workspace, in shared memory by the pair's place among the CTA's;
+        // for gate/up by token
+        const uint8_t* of = !kDown ? S.list[e] : kGlobal ? S.pair[e] : S.place[e - S.place_e];
         const int col = 2 * t;                               // the lane's accumulators' first column of a block
         DecodeScales<kScaleSmem> sc;
         if constexpr (kScaleSmem) {
@@ -523,7 +534,7 @@ __device__ __forceinline__ void DecodeWarp<kMx, kF8, kScaleSmem>::routed() {
             for (int n = 0; ok && 8 * n < n_tok; ++n) {      // blocks of eight columns: nearly always one
                 const int who = n ? column(1, g) : who0;
                 const uint32_t at = frags + who * frag_row + t * 16;
-                const uint8_t* src = kDown ? p.hq + who * (int64_t)frag_row + t * 16 : nullptr;
+                const uint8_t* src = kGlobal ? p.hq + who * (int64_t)frag_row + t * 16 : nullptr;
                 uint32_t o0 = 0, o1 = 0;                     // group sums of the lane's two columns
                 if constexpr (!kMx) {
                     o0 = (n ? column(1, col) : c00) * pieces;
@@ -536,29 +547,29 @@ __device__ __forceinline__ void DecodeWarp<kMx, kF8, kScaleSmem>::routed() {
 #pragma unroll 1
                 for (int piece = first; piece < last; ++piece, row += step) {
                     uint4 f[8];
-                    if constexpr (kDown) {
+                    if constexpr (kGlobal) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) f[i] = *reinterpret_cast<const uint4*>(src + piece * 512 + i * 64);
-                    } else if constexpr (kF8) {
+                    } else if constexpr (kF8 && !kDown) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const uint4 v = lds128(at + piece * 256 + ((i ^ (who & 3)) * 64));
+                            const uint4 v = lds128(at + piece * 256 + i * 64);
                             f[2 * i] = frag_f16<kMx>(make_uint2(v.x, v.y));
                             f[2 * i + 1] = frag_f16<kMx>(make_uint2(v.z, v.w));
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) f[i] = lds128(at + piece * 512 + ((i ^ (who & 7)) * 64));
+                        for (int i = 0; i < 8; ++i) f[i] = lds128(at + piece * 512 + i * 64);
                     }
                     float2 off0 = {}, off1 = {};
                     if constexpr (!kMx) {
                         float2 x, y;
-                        if constexpr (kDown) {
+                        if constexpr (kGlobal) {
                             x = reinterpret_cast<const float2*>(p.hsum)[o0 + piece];
                             y = reinterpret_cast<const float2*>(p.hsum)[o1 + piece];
                         } else {
-                            x = *reinterpret_cast<const float2*>(g_decode_smem + xsum + (o0 + piece) * 8);
-                            y = *reinterpret_cast<const float2*>(g_decode_smem + xsum + (o1 + piece) * 8);
+                            x = *reinterpret_cast<const float2*>(g_decode_smem + sums + (o0 + piece) * 8);
+                            y = *reinterpret_cast<const float2*>(g_decode_smem + sums + (o1 + piece) * 8);
                         }
                         off0 = make_float2(x.x, y.x);
                         off1 = make_float2(x.y, y.y);
@@ -603,28 +614,33 @@ __device__ __forceinline__ void DecodeWarp<kMx, kF8, kScaleSmem>::shared() {   /
         const int e = u / per, b = u - e * per;
         float acc[2][4] = {};
         for (int c = 0; c < R.chunks; ++c) {
-            wait_full();
-            const int first = c * R.cp, last = min(first + R.cp, R.pieces);
+            const int first = c * R.cp, n_here = min(R.cp, R.pieces - first);
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                if (8 * n >= p.T || !ok) break;
+                if (8 * n >= p.T) break;
                 const int tk = min(8 * n + g, p.T - 1);      // (an unused column takes the last token's)
-                uint32_t row = slots0 + slot * p.slot_bytes + r * 128;
-#pragma unroll 2
-                for (int piece = first; piece < last; ++piece, row += step) {
-                    uint4 v[kDown ? 2 : 1][2];
+                uint4 v[4][kDown ? 2 : 1][2];                // a chunk has at most four pieces: all loads in flight at once
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
+                        const int piece = first + min(i, n_here - 1);
                         if constexpr (kDown) {
                             const int64_t at = ((int64_t)tk * p.n_shared + e) * (p.Ns / 8) + piece * 8 + h * 4 + t;
-                            v[0][h] = reinterpret_cast<const uint4*>(p.act_hi)[at];
-                            v[1][h] = reinterpret_cast<const uint4*>(p.act_lo)[at];
+                            v[i][0][h] = reinterpret_cast<const uint4*>(p.act_hi)[at];
+                            v[i][1][h] = reinterpret_cast<const uint4*>(p.act_lo)[at];
                         } else {
-                            v[0][h] = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)tk * p.H) + piece * 8 + h * 4 + t);
+                            v[i][0][h] = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)tk * p.H) + piece * 8 + h * 4 + t);
                         }
                     }
+                if (n == 0) wait_full();
+                if (!ok) break;
+                uint32_t row = slots0 + slot * p.slot_bytes + r * 128;
 #pragma unroll
-                    for (int part = 0; part < (kDown ? 2 : 1); ++part) piece_mma_bf16(row, row + row_b, v[part], acc[n]);
+                for (int i = 0; i < 4; ++i, row += step) {
+                    if (i >= n_here) break;
+#pragma unroll
+                    for (int part = 0; part < (kDown ? 2 : 1); ++part) piece_mma_bf16(row, row + row_b, v[i][part], acc[n]);
                 }
             }
             release();
@@ -660,7 +676,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
     const uint32_t scales = ring + kDecodeWarps * p.slots * p.slot_bytes;
     const uint32_t frags = scales + kDecodeWarps * p.slots * p.scale_bytes;
     const int pieces_x = (p.H + 255) / 256, pieces_h = (p.N + 255) / 256;
-    const uint32_t xsum = frags + p.T * pieces_x * (kF8 ? 256 : 512);
+    const uint32_t row_x = frag_row_bytes<kF8>(pieces_x), row_h = frag_row_bytes<false>(pieces_h);
+    const uint32_t sums = frags + p.frag_bytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = gridDim.x, cta = blockIdx.x;
     const int T = p.T, k = p.k, P = T * k;
@@ -673,51 +690,67 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
         }
         tc::fence_mbar_init();
         S.abort = 0;
+        S.most_rows = 0;
     }
     if (warp == 1 && lane < (p.n_shared ? 6 : 3)) ws::prefetch_map(&p.map[lane]);
     for (int i = threadIdx.x; i < kMaxE / 32; i += kDecodeThreads) S.bitmap[i] = 0u;
     for (int i = threadIdx.x; i < kDecodeMaxPairs; i += kDecodeThreads) S.tokens[i] = 0u;
     if (threadIdx.x < kDecodeMaxT) S.amax[threadIdx.x] = 0u;
+    for (int i = threadIdx.x; i < T * p.H / 64; i += kDecodeThreads)   // the tokens' lines, on their way while the logits are ranked
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.x + (int64_t)i * 64));
     __syncthreads();
 
     const float* logits = p.logits;
-    if (p.wr) {   // the logits of experts c, c + G, ..: all warps an expert
+    if (p.wr) {   // the logits of experts c and c + G (then c + 2 G ..): all warps two experts
         logits = p.ws_logits;
         const int HC = p.H / 8;
-        for (int e = cta; e < p.E; e += G) {
-            const uint4* w4 = reinterpret_cast<const uint4*>(p.wr + (int64_t)e * p.H);
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                if (8 * n >= T) break;
-                float acc[8] = {};
+        for (int e = cta; e < p.E; e += 2 * G) {
+            const bool two = e + G < p.E;
+            const uint4* w0 = reinterpret_cast<const uint4*>(p.wr + (int64_t)e * p.H);
+            const uint4* w1 = reinterpret_cast<const uint4*>(p.wr + (int64_t)(two ? e + G : e) * p.H);
+#pragma unroll 1
+            for (int n = 0; 8 * n < T; ++n) {
+                float acc[2][8] = {};
+#pragma unroll 2
                 for (int c = threadIdx.x; c < HC; c += kDecodeThreads) {
-                    float wf[8];
-                    const uint4 wv = __ldg(w4 + c);
+                    float wf[2][8];
+                    const uint4 wv = __ldg(w0 + c), wu = __ldg(w1 + c);
                     uint4 xv[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         xv[j] = 8 * n + j < T ? __ldg(reinterpret_cast<const uint4*>(p.x) + (int64_t)(8 * n + j) * HC + c) : make_uint4(0u, 0u, 0u, 0u);
-                    bf16x8_to_f32(wv, wf);
+                    bf16x8_to_f32(wv, wf[0]);
+                    bf16x8_to_f32(wu, wf[1]);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
+                        if (8 * n + j >= T) break;
                         float xf[8];
                         bf16x8_to_f32(xv[j], xf);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) acc[j] = fmaf(xf[i], wf[i], acc[j]);
+                        for (int i = 0; i < 8; ++i) {
+                            acc[0][j] = fmaf(xf[i], wf[0][i], acc[0][j]);
+                            acc[1][j] = fmaf(xf[i], wf[1][i], acc[1][j]);
+                        }
                     }
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     if (8 * n + j >= T) break;
-                    const float s = warp_sum(acc[j]);
-                    if (lane == 0) S.red[(8 * n + j) * (kDecodeWarps + kDecodeStreams) + warp] = s;
+                    const float a = warp_sum(acc[0][j]), b = warp_sum(acc[1][j]);
+                    if (lane == 0) {
+                        S.red[(8 * n + j) * (kDecodeWarps + kDecodeStreams) + warp] = a;
+                        S.red[(kDecodeMaxT + 8 * n + j) * (kDecodeWarps + kDecodeStreams) + warp] = b;
+                    }
                 }
             }
             __syncthreads();
-            if (threadIdx.x < T) {
-                float s = 0.0f;
-                for (int w = 0; w < kDecodeWarps + kDecodeStreams; ++w) s += S.red[threadIdx.x * (kDecodeWarps + kDecodeStreams) + w];
-                p.ws_logits[(int64_t)threadIdx.x * p.E + e] = s;
+            if (threadIdx.x < 2 * kDecodeMaxT) {
+                const int j = threadIdx.x % kDecodeMaxT, second = threadIdx.x / kDecodeMaxT;
+                if (j < T && (two || !second)) {
+                    float s = 0.0f;
+                    for (int w = 0; w < kDecodeWarps + kDecodeStreams; ++w) s += S.red[threadIdx.x * (kDecodeWarps + kDecodeStreams) + w];
+                    p.ws_logits[(int64_t)j * p.E + e + second * G] = s;
+                }
             }
             __syncthreads();
         }
@@ -749,7 +782,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
         S.n_experts = n;
     }
     __syncthreads();
-    if (threadIdx.x < P) {
+    if (threadIdx.x < P) {       // the expert's tokens and pairs
         const int tt = threadIdx.x / k, rank = S.ids[threadIdx.x], at = __popc(S.tokens[rank] & ((1u << tt) - 1u));
         S.list[rank][at] = static_cast<uint8_t>(tt);
         S.pair[rank][at] = static_cast<uint8_t>(threadIdx.x);
@@ -778,116 +811,137 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
         else P.ph = 4;
         P.run(true);
         cg::this_grid().sync();
-        cg::this_grid().sync();
+        if (S.most_rows > p.max_rows) cg::this_grid().sync();
         P.run(false);
         cg::this_grid().sync();
         if (__any_sync(0xffffffffu, !P.ok)) give_up();
         return;
     }
     DecodeWarp<kMx, kF8, kScaleSmem> W{p, S, warp, lane, lane >> 2, lane & 3, lane_row(lane >> 2), ring + warp * p.slots * p.slot_bytes,
-                                       scales + warp * p.slots * p.scale_bytes, frags, xsum};
-    // S1 of the tokens that this CTA's experts have: their FP8 codes as B fragments (half a warp's 16 chunks of
-    // eight columns are one token's)
+                                       scales + warp * p.slots * p.scale_bytes, frags, sums};
+    // The pairs whose h the CTAs read in the down phase (units go by expert): where every CTA's fit its shared memory,
+    // each quantizes its own, and no second barrier is needed.
+    for (int c = threadIdx.x; c < G; c += kMul) {
+        const int per = p.H / 16, n = per * S.n_experts, first = share(n, c, G), end = share(n, c + 1, G);
+        int rows = 0;
+        for (int e = first / per; first < end && e * per < end; ++e) rows += __popc(S.tokens[e]);
+        atomicMax(&S.most_rows, rows);
+    }
+    if (warp == kDecodeWarps - 1) {   // this CTA's
+        const int per = S.per_expert[2], first = S.first[2], end = S.end[2];
+        int rows = 0;
+        for (int e = first / per; first < end && e * per < end; ++e) {
+            const int m = __popc(S.tokens[e]);
+            if (lane < m) {
+                S.place[e - first / per][lane] = static_cast<uint8_t>(rows + lane);
+                S.row_pair[rows + lane] = S.pair[e][lane];
+            }
+            rows += m;
+        }
+        if (lane == 0) {
+            S.place_e = first / per;
+            S.n_rows = rows;
+        }
+    }
+    // S1 of the tokens that this CTA's gate/up experts have: their FP8 codes as B fragments (half a warp's 16 chunks
+    // of eight columns are one token's).  Rolled loops: this code runs once, from a cold instruction cache.
     const int xc = p.H / 8, n_x = S.n_need * xc;
-    for (int b0 = warp * 32; b0 < n_x; b0 += 8 * kMul) {
-        const int c0 = b0 + lane;
-        uint4 v[8];
+    auto chunk_of = [&](int c, int& tk) {
+        const int o = c / xc;
+        tk = c < n_x ? S.need[o] : -1;
+        return c < n_x ? __ldg(reinterpret_cast<const uint4*>(p.x) + tk * xc + c - o * xc) : make_uint4(0u, 0u, 0u, 0u);
+    };
+#pragma unroll 2
+    for (int b0 = warp * 32; b0 < n_x; b0 += kMul) {
+        int tk;
+        float a = amax8(chunk_of(b0 + lane, tk));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = c0 + i * kMul, o = c / xc;
-            v[i] = c < n_x ? __ldg(reinterpret_cast<const uint4*>(p.x) + S.need[o] * xc + c - o * xc) : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = c0 + i * kMul;
-            float a = amax8(v[i]);
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-            if (c < n_x && (lane & 15) == 0) atomicMax(&S.amax[S.need[c / xc]], __float_as_uint(a));
-        }
+        for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        if (tk >= 0 && (lane & 15) == 0) atomicMax(&S.amax[tk], __float_as_uint(a));
     }
     multipliers_sync();
     if (threadIdx.x < T) S.sx[threadIdx.x] = __fdiv_rn(__uint_as_float(S.amax[threadIdx.x]), kFp8Max) * kDecodeLadder<kMx>;
-    for (int b0 = warp * 32; b0 < n_x; b0 += 4 * kMul) {
-        const int c0 = b0 + lane;
-        uint4 v[4];
-        int tok[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = c0 + i * kMul, o = c / xc;
-            tok[i] = c < n_x ? S.need[o] : -1;
-            v[i] = c < n_x ? __ldg(reinterpret_cast<const uint4*>(p.x) + tok[i] * xc + c - o * xc) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+    for (int b0 = warp * 32; b0 < n_x; b0 += kMul) {
+        int tk;
+        float x[8];
+        bf16x8_to_f32(chunk_of(b0 + lane, tk), x);
+        const int c8 = (b0 + lane) % xc;
+        const RowQuant s = RowQuant::of(tk >= 0 ? __uint_as_float(S.amax[tk]) : 0.0f);
+        const uint2 codes = s.codes(x);
+        int piece, i, tt;
+        frag_place<kMx>(c8, piece, i, tt);
+        if (tk >= 0) {
+            if constexpr (kF8)
+                *reinterpret_cast<uint2*>(g_decode_smem + frags + tk * row_x + piece * 256 + (i >> 1) * 64 + tt * 16 + (i & 1) * 8) =
+                    frag_order<kMx>(codes);
+            else
+                *reinterpret_cast<uint4*>(g_decode_smem + frags + tk * row_x + piece * 512 + i * 64 + tt * 16) =
+                    frag_f16<kMx>(frag_order<kMx>(codes));
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int c = c0 + u * kMul, tk = tok[u], c8 = c % xc;
-            const bool live = tk >= 0;
-            const RowQuant s = RowQuant::of(live ? __uint_as_float(S.amax[tk]) : 0.0f);
-            float x[8];
-            bf16x8_to_f32(v[u], x);
-            const uint2 codes = s.codes(x);
-            int piece, i, tt;
-            frag_place<kMx>(c8, piece, i, tt);
-            if (live) {
-                if constexpr (kF8)
-                    *reinterpret_cast<uint2*>(g_decode_smem + frags + (tk * pieces_x + piece) * 256 + (((i >> 1) ^ (tk & 3)) * 64) + tt * 16 + (i & 1) * 8) =
-                        frag_order<kMx>(codes);
-                else
-                    *reinterpret_cast<uint4*>(g_decode_smem + frags + (tk * pieces_x + piece) * 512 + ((i ^ (tk & 7)) * 64) + tt * 16) =
-                        frag_f16<kMx>(frag_order<kMx>(codes));
-            }
-            if constexpr (!kMx) {
-                const float sum = halfwarp_sum(e4m3x8_sum(codes));
-                if (live && (lane & 15) == 0)
-                    *reinterpret_cast<float*>(g_decode_smem + xsum + (tk * pieces_x * 2 + (c8 >> 4)) * 4) = sum * kNibbleOffset;
-            }
+        if constexpr (!kMx) {
+            const float sum = halfwarp_sum(e4m3x8_sum(codes));
+            if (tk >= 0 && (lane & 15) == 0)
+                *reinterpret_cast<float*>(g_decode_smem + sums + (tk * pieces_x * 2 + (c8 >> 4)) * 4) = sum * kNibbleOffset;
         }
     }
     multipliers_sync();
 
-    W.template routed<false>();
+    W.template routed<false, false>();
     if (p.n_shared) W.template shared<false>();
 
     cg::this_grid().sync();
-    // S5: pair r's codes as B fragments, by CTA r
-    for (int r = cta; r < P; r += G) {
+    // S5: rows of h as B fragments: this CTA's own pairs into shared memory, or pair r by CTA r into the workspace
+    const bool own_rows = S.most_rows <= p.max_rows;   // the same for every CTA
+    const int n_rows = own_rows ? S.n_rows : P, hc = p.N / 8;
+#pragma unroll 1
+    for (int q = own_rows ? 0 : cta, odd = 0; q < n_rows; q += own_rows ? 1 : G, odd ^= 16) {   // (the maxima of two rows in turn)
+        const int r = own_rows ? S.row_pair[q] : q;
         const float4* src = reinterpret_cast<const float4*>(p.h + (int64_t)r * p.N);
-        float a = 0.0f;
-        for (int c = threadIdx.x; c < p.N / 4; c += kMul) {
-            const float4 v = __ldcg(src + c);
-            a = fmaxf(fmaxf(a, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+        float x[8], a = 0.0f;
+        auto load = [&](int c) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f), w = v;
+            if (c < hc) { v = __ldcg(src + 2 * c); w = __ldcg(src + 2 * c + 1); }
+            x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+            x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
+        };
+#pragma unroll 1
+        for (int b0 = 0; b0 < hc; b0 += kMul) {
+            load(b0 + threadIdx.x);
+#pragma unroll
+            for (int z = 0; z < 8; ++z) a = fmaxf(a, fabsf(x[z]));
         }
         a = warp_max(a);
-        if (lane == 0) S.red[warp] = a;
+        if (lane == 0) S.red[warp + odd] = a;
         multipliers_sync();
-        const RowQuant s = RowQuant::of(warp_max(lane < kDecodeWarps ? S.red[lane] : 0.0f));
-        for (int c0 = warp * 32; c0 < p.N / 8; c0 += kMul) {
-            const int c = c0 + lane;
-            const bool live = c < p.N / 8;
-            float x[8] = {};
-            if (live) {
-                const float4 v = __ldcg(src + 2 * c), w = __ldcg(src + 2 * c + 1);
-                x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-                x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
-            }
+        const RowQuant s = RowQuant::of(warp_max(lane < kDecodeWarps ? S.red[lane + odd] : 0.0f));
+#pragma unroll 1
+        for (int b0 = 0; b0 < hc; b0 += kMul) {
+            const int c = b0 + threadIdx.x;
+            if (hc > kMul) load(c);      // else it is there already
             const uint2 codes = s.codes(x);
-            int piece, i, tt;
-            frag_place<kMx>(c, piece, i, tt);
-            if (live)
-                *reinterpret_cast<uint4*>(p.hq + ((int64_t)r * pieces_h + piece) * 512 + i * 64 + tt * 16) = frag_f16<kMx>(frag_order<kMx>(codes));
+            int piece, z, tt;
+            frag_place<kMx>(c, piece, z, tt);
+            const uint32_t at = piece * 512 + z * 64 + tt * 16;
+            uint8_t* row = own_rows ? g_decode_smem + frags + q * row_h : p.hq + (int64_t)r * row_h;
+            if (c < hc) *reinterpret_cast<uint4*>(row + at) = frag_f16<kMx>(frag_order<kMx>(codes));
             if constexpr (!kMx) {
-                const float sum = halfwarp_sum(e4m3x8_sum(codes));
-                if (live && (lane & 15) == 0) p.hsum[(int64_t)r * pieces_h * 2 + (c >> 4)] = sum * kNibbleOffset;
+                const float sum = halfwarp_sum(e4m3x8_sum(codes)) * kNibbleOffset;
+                float* to = own_rows ? reinterpret_cast<float*>(g_decode_smem + sums) + q * pieces_h * 2 : p.hsum + (int64_t)r * pieces_h * 2;
+                if (c < hc && (lane & 15) == 0) to[c >> 4] = sum;
             }
         }
-        if (threadIdx.x == 0) p.gs[r] = S.gates[r] * s.s * kDecodeLadder<kMx>;
-        multipliers_sync();
+        if (threadIdx.x == 0) (own_rows ? S.gs : p.gs)[r] = S.gates[r] * s.s * kDecodeLadder<kMx>;
     }
-    cg::this_grid().sync();
-    if (threadIdx.x < P) S.gs[threadIdx.x] = __ldcg(p.gs + threadIdx.x);
-    multipliers_sync();
-
-    W.template routed<true>();
+    if (own_rows) {
+        multipliers_sync();
+        W.template routed<true, false>();
+    } else {
+        cg::this_grid().sync();
+        if (threadIdx.x < P) S.gs[threadIdx.x] = __ldcg(p.gs + threadIdx.x);
+        multipliers_sync();
+        W.template routed<true, true>();
+    }
     if (p.n_shared) W.template shared<true>();
 
     cg::this_grid().sync();
@@ -931,7 +985,7 @@ inline DecodePlan plan_decode(const DecodeLayer& L, int64_t T, int k) {
     const size_t P = (size_t)T * k;
     p.logits = take((size_t)T * L.E * 4);
     p.h = take(P * L.N * 4);
-    p.hq = take(P * align_up(L.N, 256) * 2);                   // f16 values
+    p.hq = take(P * frag_row_bytes<false>((L.N + 255) / 256));
     p.hsum = take(P * (align_up(L.N, 256) / 128) * 4);
     p.gs = take(P * 4);
     p.act = take((size_t)T * L.n_shared * L.shared_N * 4);     // hi, then lo
@@ -973,25 +1027,33 @@ inline bool decode_map(CUtensorMap* m, const void* w, uint64_t row_bytes, uint64
 // their group sums, and the warps' rings: chunks of four pieces (8 KB) where two fit, else of two or one.  The
 // rows' scales get buffers beside the slots where they fit, else they are read in place.
 struct DecodeSmem {
-    int cp, slots, scale_bytes;
+    int cp, slots, scale_bytes, frag_bytes, max_rows;
     bool f8;
     size_t bytes;
 };
 
 inline bool plan_decode_smem(const DecodeLayer& L, int64_t T, bool mx, DecodeSmem* out) {
-    const size_t pieces = (L.H + 255) / 256, room = 227 * 1024 - sizeof(DecodeShared) - 1024 - 64;
-    const bool f8 = T * pieces * 512 > 72 * 1024;
+    const int pieces = (L.H + 255) / 256, pieces_h = (L.N + 255) / 256;
+    const size_t room = 227 * 1024 - sizeof(DecodeShared) - 1024 - 64;
+    const bool f8 = T * frag_row_bytes<false>(pieces) > 72 * 1024;
     const size_t scale = align_up((size_t)16 * std::max(L.H, L.N) / (mx ? 32 : 64), 128);
     for (int in_smem = 1; in_smem >= 0; --in_smem)
         for (int cp = 4; cp >= 1; cp >>= 1)
             for (int slots = kDecodeMaxSlots; slots >= 2; --slots) {
                 out->f8 = f8 || !in_smem;
-                const size_t fixed = T * pieces * (out->f8 ? 256 : 512) + (mx ? 0 : T * pieces * 8);
+                // room for the tokens' rows, and at least two rows of h
+                const size_t row_h = frag_row_bytes<false>(pieces_h) + (mx ? 0 : pieces_h * 8);
+                const size_t frag = align_up(std::max<size_t>(T * (out->f8 ? frag_row_bytes<true>(pieces) : frag_row_bytes<false>(pieces)),
+                                                              2 * frag_row_bytes<false>(pieces_h)), 16);
+                const size_t sums = mx ? 0 : align_up(std::max<size_t>(T * pieces * 8, frag / row_h * pieces_h * 8), 16);
+                const size_t fixed = frag + sums;
                 const size_t ring = (size_t)kDecodeWarps * slots * (cp * 2048 + (in_smem ? scale : 0));
                 if (fixed + ring > room) continue;
                 out->cp = cp;
                 out->slots = slots;
                 out->scale_bytes = in_smem ? static_cast<int>(scale) : 0;
+                out->frag_bytes = static_cast<int>(frag);
+                out->max_rows = static_cast<int>(std::min<size_t>(frag / frag_row_bytes<false>(pieces_h), mx ? 1 << 20 : sums / (pieces_h * 8)));
                 out->bytes = 1024 + fixed + ring;
                 return true;
             }
@@ -1039,6 +1101,8 @@ inline int decode_impl(const DecodeLayer& L, const uint16_t* x, const float* log
     q.slots = m.slots;
     q.slot_bytes = m.cp * 2048;
     q.scale_bytes = m.scale_bytes;
+    q.frag_bytes = m.frag_bytes;
+    q.max_rows = m.max_rows;
     q.rows[0] = decode_rows(L.H / 2, m.cp);
     q.rows[1] = decode_rows((int64_t)L.H * 2, m.cp);
     q.rows[2] = decode_rows(L.N / 2, m.cp);

@@ -81,7 +81,7 @@ struct alignas(64) DecodeParams {
     DecodeRows rows[4];           // gate/up, shared gate/up, down, shared down
     int E, H, N, k, T, n_shared, Ns;
     int slots, slot_bytes, scale_bytes;   // scale_bytes: of one of a warp's `slots` scale buffers, 0: read in place
-    int frag_bytes, max_rows;     // of the fragments in shared memory; rows of h that fit there
+    int frag_bytes, max_tokens, max_rows;   // of the fragments in shared memory; f16 rows of x and of h that fit there
     int flat;                     // bit i set: map i is 2-D (rows are not whole pieces)
 };
 
@@ -390,7 +390,8 @@ struct DecodeShared {
     float sx[kDecodeMaxT];
     float red[2 * (kDecodeWarps + kDecodeStreams) * kDecodeMaxT];
     int first[4], end[4], per_expert[4];             // this CTA's units of each phase, and how many an expert has
-    int need[kDecodeMaxT], n_need;
+    int need[kDecodeMaxT], n_need;                   // the tokens of this CTA's gate/up experts,
+    uint8_t need_at[kDecodeMaxT];                    // and a token's place among them
     uint8_t place[kDecodeMaxPairs][kDecodeMaxT];     // of expert place_e + i's pairs among the pairs of this CTA's down rows
     uint8_t row_pair[kDecodeMaxPairs];               // and those pairs
     int place_e, n_rows, most_rows;                  // n_rows of them; the most that any CTA has
@@ -476,7 +477,7 @@ struct DecodeStream {
 };
 
 // A multiplying warp.
-template <bool kMx, bool kF8, bool kScaleSmem>
+template <bool kMx, bool kScaleSmem>
 struct DecodeWarp {
     const DecodeParams& p;
     DecodeShared& S;
@@ -492,21 +493,21 @@ struct DecodeWarp {
         if (lane == 0) tc::mbar_arrive(&S.empty[warp][slot]);
         if (++slot == p.slots) { slot = 0; parity ^= 1u; }
     }
-    // kGlobal: the B fragments come from the workspace, else from shared memory.
-    template <bool kDown, bool kGlobal>
+    // The B fragments: f16 or (kF8) FP8 in shared memory, or (kGlobal) f16 in the workspace.
+    template <bool kDown, bool kGlobal, bool kF8>
     __device__ __forceinline__ void routed();
     template <bool kDown>
     __device__ __forceinline__ void shared();
 };
 
-template <bool kMx, bool kF8, bool kScaleSmem>
-template <bool kDown, bool kGlobal>
-__device__ __forceinline__ void DecodeWarp<kMx, kF8, kScaleSmem>::routed() {
+template <bool kMx, bool kScaleSmem>
+template <bool kDown, bool kGlobal, bool kF8>
+__device__ __forceinline__ void DecodeWarp<kMx, kScaleSmem>::routed() {
     constexpr int ph = kDown ? 2 : 0;
     const DecodeRows R = p.rows[ph];
     const int K = kDown ? p.N : p.H, pieces = (K + 255) / 256, per = S.per_expert[ph], end = S.end[ph];
     const uint32_t rs = kMx ? K / 32 : K / 64, step = kDown ? 2048 : 1024, row_b = kDown ? 1024u : 1024u * R.cp;
-    const uint32_t frag_row = frag_row_bytes<kF8 && !kDown>(pieces);
+    const uint32_t frag_row = frag_row_bytes<kF8>(pieces);
     for (int u = S.first[ph] + warp; u < end; u += kDecodeWarps) {
         const int e = u / per, b = u - e * per, n_tok = __popc(S.tokens[e]);
         // where the columns' fragments are: by pair in the workspace, in shared memory by the pair's place among the CTA's;
@@ -524,7 +525,10 @@ __device__ __forceinline__ void DecodeWarp<kMx, kF8, kScaleSmem>::routed() {
             sc.b = kDown ? sc.a + 8 * rs : p.scale[1] + row * rs;
         }
         // an unused column takes its block's first token: the loads coincide, and nobody reads its sums
-        auto column = [&](int n, int i) { return (int)of[8 * n + i < n_tok ? 8 * n + i : 8 * n]; };
+        auto column = [&](int n, int i) {
+            const int x = of[8 * n + i < n_tok ? 8 * n + i : 8 * n];
+            return kDown ? x : (int)S.need_at[x];
+        };
         const int who0 = column(0, g), c00 = kMx ? 0 : column(0, col), c01 = kMx ? 0 : column(0, col + 1);
         float acc[2][4] = {};
         for (int c = 0; c < R.chunks; ++c) {
@@ -550,7 +554,7 @@ __device__ __forceinline__ void DecodeWarp<kMx, kF8, kScaleSmem>::routed() {
                     if constexpr (kGlobal) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) f[i] = *reinterpret_cast<const uint4*>(src + piece * 512 + i * 64);
-                    } else if constexpr (kF8 && !kDown) {
+                    } else if constexpr (kF8) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint4 v = lds128(at + piece * 256 + i * 64);
@@ -603,9 +607,9 @@ __device__ __forceinline__ void DecodeWarp<kMx, kF8, kScaleSmem>::routed() {
     }
 }
 
-template <bool kMx, bool kF8, bool kScaleSmem>
+template <bool kMx, bool kScaleSmem>
 template <bool kDown>
-__device__ __forceinline__ void DecodeWarp<kMx, kF8, kScaleSmem>::shared() {   // bf16 weights, every token
+__device__ __forceinline__ void DecodeWarp<kMx, kScaleSmem>::shared() {   // bf16 weights, every token
     constexpr int ph = kDown ? 3 : 1;
     const DecodeRows R = p.rows[ph];
     const int per = S.per_expert[ph], end = S.end[ph];
@@ -667,7 +671,7 @@ __device__ __forceinline__ void DecodeWarp<kMx, kF8, kScaleSmem>::shared() {   /
     }
 }
 
-template <bool kMx, bool kF8, bool kScaleSmem>
+template <bool kMx, bool kScaleSmem>
 __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_constant__ DecodeParams p) {
     namespace cg = cooperative_groups;
     __shared__ DecodeShared S;
@@ -676,7 +680,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
     const uint32_t scales = ring + kDecodeWarps * p.slots * p.slot_bytes;
     const uint32_t frags = scales + kDecodeWarps * p.slots * p.scale_bytes;
     const int pieces_x = (p.H + 255) / 256, pieces_h = (p.N + 255) / 256;
-    const uint32_t row_x = frag_row_bytes<kF8>(pieces_x), row_h = frag_row_bytes<false>(pieces_h);
+    const uint32_t row_h = frag_row_bytes<false>(pieces_h);
     const uint32_t sums = frags + p.frag_bytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = gridDim.x, cta = blockIdx.x;
@@ -798,7 +802,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
             uint32_t m = 0;
             for (int e = first / per; e * per < end; ++e) m |= S.tokens[e];
             int c = 0;
-            for (; m; m &= m - 1) S.need[c++] = __ffs(m) - 1;
+            for (; m; m &= m - 1) {
+                S.need[c] = __ffs(m) - 1;
+                S.need_at[__ffs(m) - 1] = static_cast<uint8_t>(c++);
+            }
             S.n_need = c;
         }
     }
@@ -817,7 +824,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
         if (__any_sync(0xffffffffu, !P.ok)) give_up();
         return;
     }
-    DecodeWarp<kMx, kF8, kScaleSmem> W{p, S, warp, lane, lane >> 2, lane & 3, lane_row(lane >> 2), ring + warp * p.slots * p.slot_bytes,
+    DecodeWarp<kMx, kScaleSmem> W{p, S, warp, lane, lane >> 2, lane & 3, lane_row(lane >> 2), ring + warp * p.slots * p.slot_bytes,
                                        scales + warp * p.slots * p.scale_bytes, frags, sums};
     // The pairs whose h the CTAs read in the down phase (units go by expert): where every CTA's fit its shared memory,
     // each quantizes its own, and no second barrier is needed.
@@ -846,6 +853,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
     // S1 of the tokens that this CTA's gate/up experts have: their FP8 codes as B fragments (half a warp's 16 chunks
     // of eight columns are one token's).  Rolled loops: this code runs once, from a cold instruction cache.
     const int xc = p.H / 8, n_x = S.n_need * xc;
+    const bool f8 = S.n_need > p.max_tokens;   // too many for f16
+    const uint32_t row_x = f8 ? frag_row_bytes<true>(pieces_x) : frag_row_bytes<false>(pieces_x);
     auto chunk_of = [&](int c, int& tk) {
         const int o = c / xc;
         tk = c < n_x ? S.need[o] : -1;
@@ -866,28 +875,29 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
         int tk;
         float x[8];
         bf16x8_to_f32(chunk_of(b0 + lane, tk), x);
-        const int c8 = (b0 + lane) % xc;
+        const int o = (b0 + lane) / xc, c8 = b0 + lane - o * xc;
         const RowQuant s = RowQuant::of(tk >= 0 ? __uint_as_float(S.amax[tk]) : 0.0f);
         const uint2 codes = s.codes(x);
         int piece, i, tt;
         frag_place<kMx>(c8, piece, i, tt);
         if (tk >= 0) {
-            if constexpr (kF8)
-                *reinterpret_cast<uint2*>(g_decode_smem + frags + tk * row_x + piece * 256 + (i >> 1) * 64 + tt * 16 + (i & 1) * 8) =
+            if (f8)
+                *reinterpret_cast<uint2*>(g_decode_smem + frags + o * row_x + piece * 256 + (i >> 1) * 64 + tt * 16 + (i & 1) * 8) =
                     frag_order<kMx>(codes);
             else
-                *reinterpret_cast<uint4*>(g_decode_smem + frags + tk * row_x + piece * 512 + i * 64 + tt * 16) =
+                *reinterpret_cast<uint4*>(g_decode_smem + frags + o * row_x + piece * 512 + i * 64 + tt * 16) =
                     frag_f16<kMx>(frag_order<kMx>(codes));
         }
         if constexpr (!kMx) {
             const float sum = halfwarp_sum(e4m3x8_sum(codes));
             if (tk >= 0 && (lane & 15) == 0)
-                *reinterpret_cast<float*>(g_decode_smem + sums + (tk * pieces_x * 2 + (c8 >> 4)) * 4) = sum * kNibbleOffset;
+                *reinterpret_cast<float*>(g_decode_smem + sums + (o * pieces_x * 2 + (c8 >> 4)) * 4) = sum * kNibbleOffset;
         }
     }
     multipliers_sync();
 
-    W.template routed<false, false>();
+    if (f8) W.template routed<false, false, true>();
+    else W.template routed<false, false, false>();
     if (p.n_shared) W.template shared<false>();
 
     cg::this_grid().sync();
@@ -935,12 +945,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
     }
     if (own_rows) {
         multipliers_sync();
-        W.template routed<true, false>();
+        W.template routed<true, false, false>();
     } else {
         cg::this_grid().sync();
         if (threadIdx.x < P) S.gs[threadIdx.x] = __ldcg(p.gs + threadIdx.x);
         multipliers_sync();
-        W.template routed<true, true>();
+        W.template routed<true, true, false>();
     }
     if (p.n_shared) W.template shared<true>();
 
@@ -1023,46 +1033,42 @@ inline bool decode_map(CUtensorMap* m, const void* w, uint64_t row_bytes, uint64
     return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, w, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// How a CTA's 227 KB are divided: the tokens' fragments (f16, or FP8 where they would take more than a third),
-// their group sums, and the warps' rings: chunks of four pieces (8 KB) where two fit, else of two or one.  The
-// rows' scales get buffers beside the slots where they fit, else they are read in place.
+// How a CTA's 227 KB are divided: the fragments (as f16 for up to six tokens: a CTA's experts seldom have more; room
+// for all as FP8), their group sums, and the warps' rings: chunks of four pieces (8 KB) where two fit, else of two or
+// one.  The rows' scales get buffers beside the slots where they fit, else they are read in place.
 struct DecodeSmem {
-    int cp, slots, scale_bytes, frag_bytes, max_rows;
-    bool f8;
+    int cp, slots, scale_bytes, frag_bytes, max_tokens, max_rows;
     size_t bytes;
 };
 
 inline bool plan_decode_smem(const DecodeLayer& L, int64_t T, bool mx, DecodeSmem* out) {
     const int pieces = (L.H + 255) / 256, pieces_h = (L.N + 255) / 256;
     const size_t room = 227 * 1024 - sizeof(DecodeShared) - 1024 - 64;
-    const bool f8 = T * frag_row_bytes<false>(pieces) > 72 * 1024;
+    const size_t row16 = frag_row_bytes<false>(pieces), row_h = frag_row_bytes<false>(pieces_h);
     const size_t scale = align_up((size_t)16 * std::max(L.H, L.N) / (mx ? 32 : 64), 128);
-    for (int in_smem = 1; in_smem >= 0; --in_smem)
+    for (int in_smem = 1; in_smem >= 0; --in_smem) {
+        const size_t frag = std::max(std::max<size_t>(T * frag_row_bytes<true>(pieces), in_smem ? std::min<int64_t>(T, 6) * row16 : 0), 2 * row_h);
+        const size_t sums = mx ? 0 : std::max<size_t>(T * pieces, frag / row_h * pieces_h) * 8;
         for (int cp = 4; cp >= 1; cp >>= 1)
             for (int slots = kDecodeMaxSlots; slots >= 2; --slots) {
-                out->f8 = f8 || !in_smem;
-                // room for the tokens' rows, and at least two rows of h
-                const size_t row_h = frag_row_bytes<false>(pieces_h) + (mx ? 0 : pieces_h * 8);
-                const size_t frag = align_up(std::max<size_t>(T * (out->f8 ? frag_row_bytes<true>(pieces) : frag_row_bytes<false>(pieces)),
-                                                              2 * frag_row_bytes<false>(pieces_h)), 16);
-                const size_t sums = mx ? 0 : align_up(std::max<size_t>(T * pieces * 8, frag / row_h * pieces_h * 8), 16);
-                const size_t fixed = frag + sums;
                 const size_t ring = (size_t)kDecodeWarps * slots * (cp * 2048 + (in_smem ? scale : 0));
-                if (fixed + ring > room) continue;
+                if (frag + sums + ring > room) continue;
                 out->cp = cp;
                 out->slots = slots;
                 out->scale_bytes = in_smem ? static_cast<int>(scale) : 0;
                 out->frag_bytes = static_cast<int>(frag);
-                out->max_rows = static_cast<int>(std::min<size_t>(frag / frag_row_bytes<false>(pieces_h), mx ? 1 << 20 : sums / (pieces_h * 8)));
-                out->bytes = 1024 + fixed + ring;
+                out->max_tokens = static_cast<int>(frag / row16);
+                out->max_rows = static_cast<int>(frag / row_h);
+                out->bytes = 1024 + frag + sums + ring;
                 return true;
             }
+    }
     return false;
 }
 
-template <bool kMx, bool kF8, bool kScaleSmem>
+template <bool kMx, bool kScaleSmem>
 inline int launch_decode(DecodeParams& q, size_t smem, cudaStream_t stream) {
-    const void* fn = reinterpret_cast<const void*>(k_decode<kMx, kF8, kScaleSmem>);
+    const void* fn = reinterpret_cast<const void*>(k_decode<kMx, kScaleSmem>);
     if (set_smem(fn, smem)) return MOE_ERR_CUDA;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -1102,6 +1108,7 @@ inline int decode_impl(const DecodeLayer& L, const uint16_t* x, const float* log
     q.slot_bytes = m.cp * 2048;
     q.scale_bytes = m.scale_bytes;
     q.frag_bytes = m.frag_bytes;
+    q.max_tokens = m.max_tokens;
     q.max_rows = m.max_rows;
     q.rows[0] = decode_rows(L.H / 2, m.cp);
     q.rows[1] = decode_rows((int64_t)L.H * 2, m.cp);
@@ -1132,9 +1139,7 @@ inline int decode_impl(const DecodeLayer& L, const uint16_t* x, const float* log
     q.E = L.E; q.H = L.H; q.N = L.N; q.k = k; q.T = static_cast<int>(T);
     q.n_shared = L.n_shared;
     q.Ns = L.n_shared > 0 ? L.shared_N : 0;
-    return !m.scale_bytes ? launch_decode<kMx, true, false>(q, m.bytes, stream)
-           : m.f8         ? launch_decode<kMx, true, true>(q, m.bytes, stream)
-                          : launch_decode<kMx, false, true>(q, m.bytes, stream);
+    return m.scale_bytes ? launch_decode<kMx, true>(q, m.bytes, stream) : launch_decode<kMx, false>(q, m.bytes, stream);
 }
 
 inline DecodeLayer decode_layer(const moe_w4a8_layer& L) {

@@ -2,6 +2,8 @@
 //   out[m, n] = sum_b 2^(sa[m,b] + sb[n,b] - 254) sum_{k in block b} A[m,k] B[n,k]
 #pragma once
 #include "mxfp4.cuh"
+#include "route.cuh"
+#include "tc_pipe.cuh"
 
 namespace moe {
 
@@ -57,6 +59,258 @@ __global__ void __launch_bounds__(256) k_mxfp4_matmul(const uint8_t* __restrict_
         }
 }
 
+// ---- M > 16: tcgen05 -------------------------------------------------------------------------------
+//
+// kind::mxf4.block_scale takes both operands as they are stored: 128 x BN outputs a CTA, K in stages of
+// 256 codes (128-byte rows, TMA in the 128-byte swizzle), four MMAs of K = 64 a stage into one fp32
+// accumulator in TMEM, each block's two scales applied by the tensor core (products exact, fp32 sums).
+//
+// Roles: warps 0-7 drain the accumulator, 8-11 bring the scales, 12 issues the TMA loads, 13 the MMAs.
+// The scale warps read each row's eight E8M0 bytes of a stage from their rows (K / 32 bytes apart; no
+// TMA box is that narrow) and lay them out as the tensor core wants them: 512-byte blocks of 128 rows x
+// 4 scales, row r at (r % 32) 16 + (r / 32) 4, which tcgen05.cp (32x128b.warpx4) copies to four TMEM
+// columns.  The copies are issued by the MMA thread ahead of the stage's MMAs; both execute in order, so
+// one set of TMEM columns serves all stages.
+//
+// The accumulator's BN = 256 columns and the scales leave no room in TMEM for a second accumulator, so
+// the eight draining warps first take it into registers (rounded to the output type: 64 registers), free
+// it, and store while the next tile's MMAs run.
+namespace mxmm {
+
+constexpr int kThreads = 14 * 32;
+constexpr int kStageK = 256;
+
+template <int BN>
+struct Cfg {
+    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+    static constexpr int kA = 128 * 128, kB = BN * 128;
+    static constexpr int kHalves = BN > 128 ? 2 : 1;                 // 128-row blocks of B's scales
+    static constexpr int kStage = kA + kB + 3072;                    // codes, then 1 KB of A's scales and up to 2 KB of B's
+    static constexpr int kSmem = 1024 + kStages * kStage;
+};
+constexpr uint32_t kScaleColA = 256, kScaleColB = 264;               // TMEM columns: 2 x 4, 2 x 4 kHalves
+
+__device__ __forceinline__ uint32_t idesc(int n, int sf) {
+    return (static_cast<uint32_t>(sf) << 4)       // which of a column's four scales: B
+           | (1u << 7) | (1u << 10)               // A, B = E2M1
+           | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23)   // N / 8, scales UE8M0
+           | (8u << 24) | (static_cast<uint32_t>(sf) << 29);      // M / 16, A's scales
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t sa, uint32_t sb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+// 32 rows x 16 bytes of shared memory (512 contiguous bytes) -> four TMEM columns, in all four lane quadrants.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
+    uint64_t d = (saddr >> 4) & 0x3FFF;
+    d |= static_cast<uint64_t>(128 >> 4) << 16;   // core matrices (8 rows x 16 bytes) 128 bytes apart
+    d |= static_cast<uint64_t>(128 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;          // descriptor version (sm100), no swizzle
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+// Four scales (blocks b .. b + 3) of a row of `blocks`; 0 past its end.
+__device__ __forceinline__ uint32_t scales4(const uint8_t* row, int b, int blocks) {
+    if (row == nullptr || b >= blocks) return 0u;
+    if ((blocks & 3) == 0) return __ldg(reinterpret_cast<const uint32_t*>(row + b));   // rows then start at multiples of 4
+    uint32_t v = 0;
+    for (int i = 0; i < 4 && b + i < blocks; ++i) v |= static_cast<uint32_t>(__ldg(row + b + i)) << (8 * i);
+    return v;
+}
+
+template <int BN, int kType>
+__global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                                                      const uint8_t* __restrict__ as, const uint8_t* __restrict__ bs, int M, int N, int K,
+                                                      void* __restrict__ out) {
+    using C = Cfg<BN>;
+    extern __shared__ __align__(16) uint8_t raw[];
+    __shared__ uint64_t full[C::kStages], scaled[C::kStages], empty[C::kStages], acc_full, acc_empty;
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int abort;
+    const uint32_t base = (tc::smem_u32(raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tn = (N + BN - 1) / BN, tiles = (M + 127) / 128 * tn, stages = (K + kStageK - 1) / kStageK, blocks = K / kMxBlock;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&scaled[i], 4);
+            tc::mbar_init(&empty[i], 1);
+        }
+        tc::mbar_init(&acc_full, 1);
+        tc::mbar_init(&acc_empty, 8);
+        tc::fence_mbar_init();
+        abort = 0;
+    }
+    if (warp == 0) tc::tmem_alloc(&tmem_slot, 512);
+    if (warp == 12 && lane == 0) {
+        ws::prefetch_map(&map_a);
+        ws::prefetch_map(&map_b);
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    bool ok = true;
+
+    if (warp == 12) {
+        if (lane == 0) {
+            ws::Ring<C::kStages> r;
+            for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+                const int m0 = tile / tn * 128, n0 = tile % tn * BN;
+                for (int s = 0; s < stages; ++s, r.next()) {
+                    if (!(ok = ws::wait(&empty[r.idx], r.phase ^ 1u, &abort))) break;
+                    tc::mbar_arrive_expect_tx(&full[r.idx], C::kA + C::kB);
+                    uint8_t* dst = raw + (base - tc::smem_u32(raw)) + r.idx * C::kStage;
+                    ws::tma_load_2d(dst, &map_a, s * 128, m0, &full[r.idx]);
+                    ws::tma_load_2d(dst + C::kA, &map_b, s * 128, n0, &full[r.idx]);
+                }
+            }
+        }
+    } else if (warp == 13) {
+        if (lane == 0) {
+            ws::Ring<C::kStages> r;
+            uint32_t phase = 0;
+            for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, phase ^= 1u) {
+                ok = ws::wait(&acc_empty, phase ^ 1u, &abort);
+                tc::tc_fence_after();
+                for (int s = 0; ok && s < stages; ++s, r.next()) {
+                    ok = ws::wait(&full[r.idx], r.phase, &abort) && ws::wait(&scaled[r.idx], r.phase, &abort);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    const uint32_t a = base + r.idx * C::kStage, sf = a + C::kA + C::kB;
+#pragma unroll
+                    for (int kb = 0; kb < 2; ++kb) {
+                        copy_scales(tmem + kScaleColA + 4 * kb, sf + 512 * kb);
+#pragma unroll
+                        for (int h = 0; h < C::kHalves; ++h)
+                            copy_scales(tmem + kScaleColB + 4 * (kb * C::kHalves + h), sf + 1024 + 512 * (kb * C::kHalves + h));
+                    }
+                    const uint64_t da = tc::sdesc_sw128(a), db = tc::sdesc_sw128(a + C::kA);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (s * kStageK + 64 * j >= K) break;
+                        mma(tmem, da + 2 * j, db + 2 * j, idesc(BN, 2 * (j & 1)), tmem + kScaleColA + 4 * (j >> 1),
+                            tmem + kScaleColB + 4 * C::kHalves * (j >> 1), s > 0 || j > 0);
+                    }
+                    tc::mma_commit(&empty[r.idx]);
+                }
+                if (ok) tc::mma_commit(&acc_full);
+            }
+        }
+    } else if (warp >= 8) {
+        const int w = warp - 8;
+        ws::Ring<C::kStages> r;
+        for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+            const int m = tile / tn * 128 + 32 * w + lane, n = tile % tn * BN + 32 * w + lane;
+            const uint8_t* rows[1 + C::kHalves];
+            rows[0] = m < M ? as + (int64_t)m * blocks : nullptr;
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h) rows[1 + h] = n + 128 * h < N ? bs + (int64_t)(n + 128 * h) * blocks : nullptr;
+            uint32_t v[1 + C::kHalves][2];
+            auto load = [&](int s) {
+#pragma unroll
+                for (int i = 0; i < 1 + C::kHalves; ++i)
+#pragma unroll
+                    for (int kb = 0; kb < 2; ++kb) v[i][kb] = scales4(rows[i], s * 8 + 4 * kb, blocks);
+            };
+            load(0);
+            for (int s = 0; s < stages; ++s, r.next()) {
+                if (!(ok = ws::wait(&empty[r.idx], r.phase ^ 1u, &abort))) break;
+                uint8_t* sf = raw + (base - tc::smem_u32(raw)) + r.idx * C::kStage + C::kA + C::kB + lane * 16 + w * 4;
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    *reinterpret_cast<uint32_t*>(sf + 512 * kb) = v[0][kb];
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+                        *reinterpret_cast<uint32_t*>(sf + 1024 + 512 * (kb * C::kHalves + h)) = v[1 + h][kb];
+                }
+                if (s + 1 < stages) load(s + 1);
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&scaled[r.idx]);
+            }
+        }
+    } else {
+        constexpr int kCols = BN / 2;
+        const int q = warp & 3, c0 = (warp >> 2) * kCols;
+        uint32_t phase = 0;
+        for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, phase ^= 1u) {
+            if (!(ok = ws::wait(&acc_full, phase, &abort))) break;
+            tc::tc_fence_after();
+            uint32_t v[kType == MOE_F32 ? kCols : kCols / 2];
+#pragma unroll
+            for (int c = 0; c < kCols; c += 32) {
+                uint32_t t[32];
+                tc::tmem_ld32(tmem + (static_cast<uint32_t>(q * 32) << 16) + c0 + c, t);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    if constexpr (kType == MOE_F32) v[c + i] = t[i];
+                    else if (i & 1)
+                        v[(c + i) >> 1] = static_cast<uint32_t>(f32_to_bf16_bits(__uint_as_float(t[i - 1]))) |
+                                          (static_cast<uint32_t>(f32_to_bf16_bits(__uint_as_float(t[i]))) << 16);
+                }
+            }
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&acc_empty);
+            const int64_t m = tile / tn * 128 + q * 32 + lane;
+            const int n0 = tile % tn * BN + c0;
+            if (m < M) {
+                constexpr int kElem = kType == MOE_F32 ? 4 : 2, kVec = 16 / kElem;
+                uint8_t* o = static_cast<uint8_t*>(out) + (m * N + n0) * kElem;
+                if (N % kVec == 0) {
+#pragma unroll
+                    for (int c = 0; c < kCols; c += kVec)
+                        if (n0 + c < N)
+                            *reinterpret_cast<uint4*>(o + c * kElem) =
+                                make_uint4(v[c * kElem / 4], v[c * kElem / 4 + 1], v[c * kElem / 4 + 2], v[c * kElem / 4 + 3]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c)
+                        if (n0 + c < N) {
+                            if constexpr (kType == MOE_F32) reinterpret_cast<uint32_t*>(o)[c] = v[c];
+                            else reinterpret_cast<uint16_t*>(o)[c] = static_cast<uint16_t>(v[c >> 1] >> (16 * (c & 1)));
+                        }
+                }
+            }
+        }
+    }
+    if (!ok) atomicOr(&g_device_status, kStatusTimeout);
+    __syncwarp();
+    tc::tc_fence_before();
+    __syncthreads();
+    if (abort) {   // copies and MMAs in flight (microseconds) end before the CTA does
+        const uint64_t t0 = tc::globaltimer_ns();
+        while (tc::globaltimer_ns() - t0 < 10000000ull) __nanosleep(100000);
+    }
+    tc::tc_fence_after();
+    if (warp == 0) {
+        tc::tmem_relinquish();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int BN, int kType>
+inline int launch(const uint8_t* a, const uint8_t* as, const uint8_t* b, const uint8_t* bs, int M, int N, int K, void* out, int sms,
+                  cudaStream_t stream) {
+    CUtensorMap ma, mb;
+    if (!make_map_u8(&ma, a, K / 2, M, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map_u8(&mb, b, K / 2, N, 128, BN, CU_TENSOR_MAP_SWIZZLE_128B))
+        return MOE_ERR_CUDA;
+    if (set_smem(reinterpret_cast<const void*>(k_gemm<BN, kType>), Cfg<BN>::kSmem)) return MOE_ERR_CUDA;
+    const int64_t tiles = (int64_t)((M + 127) / 128) * ((N + BN - 1) / BN);
+    k_gemm<BN, kType><<<static_cast<unsigned>(std::min<int64_t>(tiles, sms)), kThreads, Cfg<BN>::kSmem, stream>>>(ma, mb, as, bs, M, N, K, out);
+    return launch_status();
+}
+
+}  // namespace mxmm
+
 }  // namespace moe
 
 extern "C" int mxfp4_matmul(const uint8_t* a, const uint8_t* a_scales, const uint8_t* b, const uint8_t* b_scales,
@@ -69,6 +323,19 @@ extern "C" int mxfp4_matmul(const uint8_t* a, const uint8_t* a_scales, const uin
     if (!a || !a_scales || !b || !b_scales || !out) return MOE_ERR_INVALID_ARG;
     if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_scales, 4) || !aligned(b_scales, 4) || !aligned(out, 16))
         return MOE_ERR_MISALIGNED;
+    if (M > 16) {
+        int dev = 0, sms = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        const int m = (int)M, n = (int)N, k = (int)K;
+        // the widest tile that gives every SM one
+        const int64_t rows = (M + 127) / 128;
+        const int bn = rows * ((N + 255) / 256) >= sms ? 256 : rows * ((N + 127) / 128) >= sms ? 128 : 64;
+#define MOE_MM(BN, TYPE) mxmm::launch<BN, TYPE>(a, a_scales, b, b_scales, m, n, k, out, sms, stream)
+        if (out_type == MOE_F32) return bn == 256 ? MOE_MM(256, MOE_F32) : bn == 128 ? MOE_MM(128, MOE_F32) : MOE_MM(64, MOE_F32);
+        return bn == 256 ? MOE_MM(256, MOE_BF16) : bn == 128 ? MOE_MM(128, MOE_BF16) : MOE_MM(64, MOE_BF16);
+#undef MOE_MM
+    }
     const dim3 grid(static_cast<unsigned>((N + 63) / 64), static_cast<unsigned>((M + 63) / 64));
     if (grid.y > 65535) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (out_type == MOE_F32)

@@ -82,11 +82,11 @@ constexpr int kStageK = 256;
 
 template <int BN>
 struct Cfg {
-    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 5 : 7;
     static constexpr int kA = 128 * 128, kB = BN * 128;
     static constexpr int kHalves = BN > 128 ? 2 : 1;                 // 128-row blocks of B's scales
     static constexpr int kStage = kA + kB + 3072;                    // codes, then 1 KB of A's scales and up to 2 KB of B's
-    static constexpr int kSmem = 1024 + kStages * kStage;
+    static constexpr int kSmem = 1024 + kStages * kStage + 8 * 2048;   // and the draining warps' buffers
 };
 constexpr uint32_t kScaleColA = 256, kScaleColB = 264;               // TMEM columns: 2 x 4, 2 x 4 kHalves
 
@@ -113,13 +113,22 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
 
-// Four scales (blocks b .. b + 3) of a row of `blocks`; 0 past its end.
-__device__ __forceinline__ uint32_t scales4(const uint8_t* row, int b, int blocks) {
-    if (row == nullptr || b >= blocks) return 0u;
-    if ((blocks & 3) == 0) return __ldg(reinterpret_cast<const uint32_t*>(row + b));   // rows then start at multiples of 4
-    uint32_t v = 0;
-    for (int i = 0; i < 4 && b + i < blocks; ++i) v |= static_cast<uint32_t>(__ldg(row + b + i)) << (8 * i);
-    return v;
+// Sixteen scales (blocks b .. b + 15) of a row of `blocks`; 0 past its end.  One 16-byte load where rows are
+// multiples of 16 blocks: loads of many rows cost their sectors, and this halves or quarters them.
+__device__ __forceinline__ uint4 scales16(const uint8_t* row, int b, int blocks) {
+    if (row == nullptr || b >= blocks) return make_uint4(0u, 0u, 0u, 0u);
+    if ((blocks & 15) == 0) return __ldg(reinterpret_cast<const uint4*>(row + b));
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+    if ((blocks & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (b + 4 * i < blocks) v[i] = __ldg(reinterpret_cast<const uint32_t*>(row + b) + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < 4 && b + 4 * i + j < blocks; ++j) v[i] |= static_cast<uint32_t>(__ldg(row + b + 4 * i + j)) << (8 * j);
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 template <int BN, int kType>
@@ -211,28 +220,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
             rows[0] = m < M ? as + (int64_t)m * blocks : nullptr;
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h) rows[1 + h] = n + 128 * h < N ? bs + (int64_t)(n + 128 * h) * blocks : nullptr;
-            uint32_t v[1 + C::kHalves][2];
-            auto load = [&](int s) {
+            constexpr int kAhead = 2;   // pairs of stages whose scales are on their way
+            uint4 v[kAhead][1 + C::kHalves];
+            auto load = [&](int pair, uint4 (&to)[1 + C::kHalves]) {
 #pragma unroll
-                for (int i = 0; i < 1 + C::kHalves; ++i)
-#pragma unroll
-                    for (int kb = 0; kb < 2; ++kb) v[i][kb] = scales4(rows[i], s * 8 + 4 * kb, blocks);
+                for (int i = 0; i < 1 + C::kHalves; ++i) to[i] = scales16(rows[i], pair * 16, blocks);
             };
-            load(0);
-            for (int s = 0; s < stages; ++s, r.next()) {
-                if (!(ok = ws::wait(&empty[r.idx], r.phase ^ 1u, &abort))) break;
-                uint8_t* sf = raw + (base - tc::smem_u32(raw)) + r.idx * C::kStage + C::kA + C::kB + lane * 16 + w * 4;
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    *reinterpret_cast<uint32_t*>(sf + 512 * kb) = v[0][kb];
+            for (int d = 0; d < kAhead; ++d) load(d, v[d]);
+            for (int s0 = 0; ok && s0 < stages; s0 += 2 * kAhead) {
 #pragma unroll
-                    for (int h = 0; h < C::kHalves; ++h)
-                        *reinterpret_cast<uint32_t*>(sf + 1024 + 512 * (kb * C::kHalves + h)) = v[1 + h][kb];
+                for (int d = 0; d < 2 * kAhead; ++d) {
+                    const int s = s0 + d;
+                    if (s >= stages || !(ok = ws::wait(&empty[r.idx], r.phase ^ 1u, &abort))) break;
+                    uint8_t* sf = raw + (base - tc::smem_u32(raw)) + r.idx * C::kStage + C::kA + C::kB + lane * 16 + w * 4;
+#pragma unroll
+                    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                        for (int i = 0; i < 1 + C::kHalves; ++i) {
+                            const uint4& q = v[d >> 1][i];
+                            *reinterpret_cast<uint32_t*>(sf + (i ? 1024 + 512 * (kb * C::kHalves + i - 1) : 512 * kb)) =
+                                d & 1 ? (kb ? q.w : q.z) : (kb ? q.y : q.x);
+                        }
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&scaled[r.idx]);
+                    if (d & 1) load(s / 2 + kAhead, v[d >> 1]);
+                    r.next();
                 }
-                if (s + 1 < stages) load(s + 1);
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&scaled[r.idx]);
             }
         }
     } else {
@@ -259,25 +274,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&acc_empty);
-            const int64_t m = tile / tn * 128 + q * 32 + lane;
-            const int n0 = tile % tn * BN + c0;
-            if (m < M) {
-                constexpr int kElem = kType == MOE_F32 ? 4 : 2, kVec = 16 / kElem;
-                uint8_t* o = static_cast<uint8_t*>(out) + (m * N + n0) * kElem;
-                if (N % kVec == 0) {
+            const int m0 = tile / tn * 128 + q * 32, n0 = tile % tn * BN + c0;
+            constexpr int kElem = kType == MOE_F32 ? 4 : 2, kVec = 16 / kElem;
+            if (N % kVec == 0) {
+                // 64 bytes of each of the 32 rows at a time through shared memory, so that a store writes whole rows'
+                // segments (chunk c of row l at c ^ (l / 2) % 4: no bank conflicts either way)
+                uint8_t* buf = raw + (base - tc::smem_u32(raw)) + C::kStages * C::kStage + warp * 2048;
 #pragma unroll
-                    for (int c = 0; c < kCols; c += kVec)
-                        if (n0 + c < N)
-                            *reinterpret_cast<uint4*>(o + c * kElem) =
-                                make_uint4(v[c * kElem / 4], v[c * kElem / 4 + 1], v[c * kElem / 4 + 2], v[c * kElem / 4 + 3]);
-                } else {
+                for (int c = 0; c < kCols * kElem / 64; ++c) {
+                    __syncwarp();
 #pragma unroll
-                    for (int c = 0; c < kCols; ++c)
-                        if (n0 + c < N) {
-                            if constexpr (kType == MOE_F32) reinterpret_cast<uint32_t*>(o)[c] = v[c];
-                            else reinterpret_cast<uint16_t*>(o)[c] = static_cast<uint16_t>(v[c >> 1] >> (16 * (c & 1)));
-                        }
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4*>(buf + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+                            make_uint4(v[16 * c + 4 * i], v[16 * c + 4 * i + 1], v[16 * c + 4 * i + 2], v[16 * c + 4 * i + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = i * 8 + (lane >> 2), n = n0 + (64 / kElem) * c + (lane & 3) * kVec;
+                        const uint4 x = *reinterpret_cast<const uint4*>(buf + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
+                        if (m0 + row < M && n < N)
+                            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + ((int64_t)(m0 + row) * N + n) * kElem) = x;
+                    }
                 }
+            } else if (m0 + lane < M) {
+                uint8_t* o = static_cast<uint8_t*>(out) + ((int64_t)(m0 + lane) * N + n0) * kElem;
+#pragma unroll
+                for (int c = 0; c < kCols; ++c)
+                    if (n0 + c < N) {
+                        if constexpr (kType == MOE_F32) reinterpret_cast<uint32_t*>(o)[c] = v[c];
+                        else reinterpret_cast<uint16_t*>(o)[c] = static_cast<uint16_t>(v[c >> 1] >> (16 * (c & 1)));
+                    }
             }
         }
     }

@@ -681,65 +681,80 @@ def moe_hybrid_forward_profiled(layer: LayerH, x, logits, k: int, out, ws, event
 
 
 # ---- MXFP4 rows and experts ---------------------------------------------------------------------
+#
+# These calls take a few microseconds of GPU time at decoding sizes, so their marshalling is kept short: torch and the
+# entry points are looked up once, tensors are checked by plain attribute tests.
 
-def _dtype_code(dtype) -> int:
-    """moe_dtype of a torch dtype."""
-    import torch
-    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(dtype)
+_fast = None
+
+
+def _entry():
+    """(torch, the library, {torch dtype: moe_dtype}), looked up once."""
+    global _fast
+    if _fast is None:
+        import torch
+        _fast = (torch, lib(), {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    return _fast
+
+
+def _dtype_code(codes, dtype) -> int:
+    code = codes.get(dtype)
     if code is None:
         raise ValueError(f"expected bfloat16, float16 or float32, got {dtype}")
     return code
 
 
-def _want(t, name: str, dtype, *shape):
+def _want(t, name: str, dev: int, dtype, shape) -> int:
     """The tensor's device pointer, once its type, shape, device and layout are as the call reads it."""
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    return _here(t, name)
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous {dtype} {list(shape)} on the current CUDA device ({dev}), "
+                     f"got {t.dtype} {list(t.shape)} on {t.device}")
 
 
-def _here(t, name: str):
-    import torch
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name}: expected a tensor on the current CUDA device, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
-    return t.data_ptr()
+def _stream_of(torch, stream, dev: int) -> int:
+    """The handle of a stream (torch stream or int), of the current one for None."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def mxfp4_quant_rows(x, codes, scales, stream=None) -> None:
     """x bf16 / f16 / fp32 [rows, K] (rows may be strided) -> codes uint8 [rows, K/2], E8M0 scales
     uint8 [rows, K/32]."""
-    import torch
+    torch, L, dtypes = _entry()
+    dev, u8 = torch._C._cuda_getDevice(), torch.uint8
     rows, K = x.shape
-    if x.stride(1) != 1 and K > 1:
-        raise ValueError("x: expected rows with consecutive columns")
-    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
-        raise ValueError(f"x: expected a tensor on the current CUDA device, got {x.device}")
-    _check(lib().mxfp4_quant_rows(x.data_ptr(), _dtype_code(x.dtype), rows, K, x.stride(0),
-                                  _want(codes, "codes", torch.uint8, rows, K // 2),
-                                  _want(scales, "scales", torch.uint8, rows, K // 32),
-                                  _stream(stream)), "mxfp4_quant_rows")
+    stride, step = x.stride()
+    if x.get_device() != dev or (step != 1 and K > 1):
+        raise ValueError(f"x: expected rows with consecutive columns on the current CUDA device ({dev}), got strides "
+                         f"{x.stride()} on {x.device}")
+    _check(L.mxfp4_quant_rows(x.data_ptr(), _dtype_code(dtypes, x.dtype), rows, K, stride,
+                              _want(codes, "codes", dev, u8, (rows, K // 2)),
+                              _want(scales, "scales", dev, u8, (rows, K // 32)),
+                              _stream_of(torch, stream, dev)), "mxfp4_quant_rows")
 
 
 def mxfp4_dequant_rows(codes, scales, y, stream=None) -> None:
     """codes uint8 [rows, K/2], scales uint8 [rows, K/32] -> y bf16 / fp32 [rows, K]."""
-    import torch
+    torch, L, dtypes = _entry()
+    dev, u8 = torch._C._cuda_getDevice(), torch.uint8
     rows, K = y.shape
-    _check(lib().mxfp4_dequant_rows(_want(codes, "codes", torch.uint8, rows, K // 2),
-                                    _want(scales, "scales", torch.uint8, rows, K // 32), rows, K, _here(y, "y"),
-                                    _dtype_code(y.dtype), _stream(stream)), "mxfp4_dequant_rows")
+    _check(L.mxfp4_dequant_rows(_want(codes, "codes", dev, u8, (rows, K // 2)),
+                                _want(scales, "scales", dev, u8, (rows, K // 32)), rows, K,
+                                _want(y, "y", dev, y.dtype, (rows, K)), _dtype_code(dtypes, y.dtype),
+                                _stream_of(torch, stream, dev)), "mxfp4_dequant_rows")
 
 
 def mxfp4_matmul(a, a_scales, b, b_scales, out, stream=None) -> None:
     """out bf16 / fp32 [M, N] = A B^T over MXFP4 rows a uint8 [M, K/2], b uint8 [N, K/2]."""
-    import torch
-    M, N, K = a.shape[0], b.shape[0], 2 * a.shape[1]
-    u8 = torch.uint8
-    _check(lib().mxfp4_matmul(_want(a, "a", u8, M, K // 2), _want(a_scales, "a_scales", u8, M, K // 32),
-                              _want(b, "b", u8, N, K // 2), _want(b_scales, "b_scales", u8, N, K // 32), M, N, K,
-                              _want(out, "out", out.dtype, M, N), _dtype_code(out.dtype), _stream(stream)),
-           "mxfp4_matmul")
+    torch, L, dtypes = _entry()
+    dev, u8 = torch._C._cuda_getDevice(), torch.uint8
+    (M, half), N = a.shape, b.shape[0]
+    _check(L.mxfp4_matmul(_want(a, "a", dev, u8, (M, half)), _want(a_scales, "a_scales", dev, u8, (M, half // 16)),
+                          _want(b, "b", dev, u8, (N, half)), _want(b_scales, "b_scales", dev, u8, (N, half // 16)),
+                          M, N, 2 * half, _want(out, "out", dev, out.dtype, (M, N)), _dtype_code(dtypes, out.dtype),
+                          _stream_of(torch, stream, dev)), "mxfp4_matmul")
 
 
 @dataclass
@@ -793,39 +808,51 @@ def moe_mxfp4_decode_workspace_bytes(layer, T: int, k: int) -> int:
     return int(lib().moe_mxfp4_decode_workspace_bytes(ctypes.byref(s), T, k))
 
 
-def _decode(fn, where: str, layer, x, routing, routing_dtype, routing_rows, k, out, ws, stream):
-    import torch
-    T, H = x.shape[0], layer.H
-    s = layer.c_struct()
-    _check(fn(ctypes.byref(s), _want(x, "x", torch.bfloat16, T, H),
-              _want(routing, "routing", routing_dtype, *routing_rows), T, k,
-              _want(out, "out", torch.bfloat16, T, H), _here(ws, "ws"), ws.numel() * ws.element_size(),
-              _stream(stream)), where)
+def _weights(dev, E, H, N, gate, up, down, dtype, per):
+    """The pointers of stacked expert projections gate / up [E, N, H / per] and down [E, H, N / per]."""
+    rows = (E, N, H // per)
+    return (_want(gate, "gate", dev, dtype, rows), _want(up, "up", dev, dtype, rows),
+            _want(down, "down", dev, dtype, (E, H, N // per)))
+
+
+def _decode(name: str, layer, x, routing, router: bool, k: int, out, ws, stream):
+    torch, L, _ = _entry()
+    dev, bf16 = torch._C._cuda_getDevice(), torch.bfloat16
+    E, H, N, T = layer.E, layer.H, layer.N, x.shape[0]
+    shared = (0, 0, None, None, None)
+    if layer.sh_gate is not None:
+        n, Ns = layer.n_shared, layer.shared_N
+        shared = (n, Ns) + _weights(dev, n, H, Ns, layer.sh_gate, layer.sh_up, layer.sh_down, bf16, 1)
+    if name == "w4a8":
+        s = _CLayer(E, H, N, layer.group,
+                    *_weights(dev, E, H, N, layer.gate_packed, layer.up_packed, layer.down_packed, torch.int32, 8),
+                    *_weights(dev, E, H, N, layer.gate_scales, layer.up_scales, layer.down_scales, bf16, 128), *shared)
+        fn = L.moe_w4a8_decode_router if router else L.moe_w4a8_decode
+    else:
+        u8 = torch.uint8
+        s = _CLayerMX(E, H, N, *_weights(dev, E, H, N, layer.gate_f4, layer.up_f4, layer.down_f4, u8, 2),
+                      *_weights(dev, E, H, N, layer.gate_e8, layer.up_e8, layer.down_e8, u8, 32), *shared)
+        fn = L.moe_mxfp4_decode_router if router else L.moe_mxfp4_decode
+    routed = _want(routing, "wr", dev, bf16, (E, H)) if router else _want(routing, "logits", dev, torch.float32, (T, E))
+    _check(fn(ctypes.byref(s), _want(x, "x", dev, bf16, (T, H)), routed, T, k, _want(out, "out", dev, bf16, (T, H)),
+              _want(ws, "ws", dev, ws.dtype, ws.shape), ws.nbytes, _stream_of(torch, stream, dev)), fn.__name__)
 
 
 def moe_w4a8_decode(layer: Layer, x, logits, k: int, out, ws, stream=None) -> None:
     """out bf16 [T, H] = the W4A8 layer (+ shared experts) on x bf16 [T <= 16, H], logits fp32 [T, E]."""
-    import torch
-    _decode(lib().moe_w4a8_decode, "moe_w4a8_decode", layer, x, logits, torch.float32, (x.shape[0], layer.E), k, out,
-            ws, stream)
+    _decode("w4a8", layer, x, logits, False, k, out, ws, stream)
 
 
 def moe_w4a8_decode_router(layer: Layer, x, wr, k: int, out, ws, stream=None) -> None:
     """moe_w4a8_decode fed by the router weight wr bf16 [E, H]."""
-    import torch
-    _decode(lib().moe_w4a8_decode_router, "moe_w4a8_decode_router", layer, x, wr, torch.bfloat16,
-            (layer.E, layer.H), k, out, ws, stream)
+    _decode("w4a8", layer, x, wr, True, k, out, ws, stream)
 
 
 def moe_mxfp4_decode(layer: LayerMX, x, logits, k: int, out, ws, stream=None) -> None:
     """out bf16 [T, H] = the layer with MXFP4 experts on x bf16 [T <= 16, H], logits fp32 [T, E]."""
-    import torch
-    _decode(lib().moe_mxfp4_decode, "moe_mxfp4_decode", layer, x, logits, torch.float32, (x.shape[0], layer.E), k, out,
-            ws, stream)
+    _decode("mxfp4", layer, x, logits, False, k, out, ws, stream)
 
 
 def moe_mxfp4_decode_router(layer: LayerMX, x, wr, k: int, out, ws, stream=None) -> None:
     """moe_mxfp4_decode fed by the router weight wr bf16 [E, H]."""
-    import torch
-    _decode(lib().moe_mxfp4_decode_router, "moe_mxfp4_decode_router", layer, x, wr, torch.bfloat16,
-            (layer.E, layer.H), k, out, ws, stream)
+    _decode("mxfp4", layer, x, wr, True, k, out, ws, stream)

@@ -85,16 +85,6 @@ struct alignas(64) DecodeParams {
     int flat;                     // bit i set: map i is 2-D (rows are not whole pieces)
 };
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1, float c0, float c1, float c2, float c3) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
-}
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-    mma_f16(d, a0, a1, a2, a3, b0, b1, d[0], d[1], d[2], d[3]);
-}
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -110,23 +100,6 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 
 // Row g of an MMA's eight is row lane_row() of the eight in shared memory: eight consecutive lanes (two g) then
 // read rows whose swizzle differs in bit 2, so a 16-byte load of four neighbouring chunks of each has no bank conflict.
 __device__ __forceinline__ int lane_row(int g) { return (g >> 1) | ((g & 1) << 2); }
-// Four E8M0 bytes -> four floats.
-__device__ __forceinline__ void e8m0x4_to_f32(uint32_t b, float (&s)[4]) {
-    uint32_t lo, hi;
-    asm("{\n\t.reg .b16 h0, h1;\n\tmov.b32 {h0, h1}, %2;\n\tcvt.rn.bf16x2.ue8m0x2 %0, h0;\n\tcvt.rn.bf16x2.ue8m0x2 %1, h1;\n\t}"
-        : "=r"(lo), "=r"(hi) : "r"(b));
-    s[0] = __uint_as_float(lo << 16);
-    s[1] = __uint_as_float(lo & 0xFFFF0000u);
-    s[2] = __uint_as_float(hi << 16);
-    s[3] = __uint_as_float(hi & 0xFFFF0000u);
-}
-// Eight E2M1 codes -> four f16x2 in order.
-__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\tcvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
-}
-
 // Eight codes in column order -> the order in which the weights' widening pairs them: for INT4 the
 // nibbles of a word come out as (0,4) (1,5) (2,6) (3,7), for MXFP4 as they are.
 template <bool kMx>

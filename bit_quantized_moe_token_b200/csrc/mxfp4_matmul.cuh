@@ -7,57 +7,120 @@
 
 namespace moe {
 
-// 64 x 64 outputs a CTA, K in blocks of 32: both tiles are widened to fp32 in shared memory and
-// each thread sums a 4 x 4 patch.
-template <int kType>
-__global__ void __launch_bounds__(256) k_mxfp4_matmul(const uint8_t* __restrict__ a, const uint8_t* __restrict__ as,
-                                                       const uint8_t* __restrict__ b, const uint8_t* __restrict__ bs,
-                                                       int64_t M, int64_t N, int K, void* __restrict__ out) {
-    __shared__ float ta[kMxBlock][65], tb[kMxBlock][65];
-    const int64_t m0 = (int64_t)blockIdx.y * 64, n0 = (int64_t)blockIdx.x * 64;
-    const int row = threadIdx.x >> 2, part = threadIdx.x & 3;   // a row's block: 4 threads x 4 bytes
-    const int tm = threadIdx.x >> 4, tn = threadIdx.x & 15;
-    float acc[4][4] = {};
-    for (int blk = 0; blk < K / kMxBlock; ++blk) {
-        __syncthreads();
+// ---- M <= 16: mma.sync ----------------------------------------------------------------------------
+//
+// A few tokens' product is the reading of B.  A CTA takes 16 rows of B (the MMA's M = 16; tokens are its N = 8
+// columns, in one or two blocks) and its eight warps 512 columns at a time each; a warp asks for all of its codes
+// and scales at once and for the next 512 columns' before it multiplies, so B streams in with one latency, and the
+// warps' sums meet in shared memory in a fixed order.  Word t of a 16-byte block goes to lane t of a row's four, so an
+// MMA pair covers one block; E2M1 is exact in f16.  A block's sum is a multiple of 1/4 below 2^11: multiplied first by
+// the smaller of its two scales it neither overflows (unless the result does) nor loses bits, and a scale of 255 (NaN,
+// the largest as bits too) stays what it is.
+// Tokens beyond 16 go to the tensor-memory kernel, which reads 128 rows of A whatever M is.
+namespace mxmm {
+
+// Sixteen scales (blocks b .. b + 15) of a row of `blocks`; 0 past its end.  One 16-byte load where the row allows it:
+// loads of many rows cost their sectors, and this halves or quarters them.
+__device__ __forceinline__ uint4 scales16(const uint8_t* row, int b, int blocks) {
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+    if (row != nullptr && b < blocks) {
+        const uint8_t* at = row + b;
+        const int n = blocks - b;   // scales left in the row
+        const uint32_t low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at));
+        if (n >= 16 && (low & 15u) == 0) return __ldg(reinterpret_cast<const uint4*>(at));
+        if (n >= 16 && (low & 3u) == 0) {
 #pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            const int64_t r = (side ? n0 : m0) + row;
-            uint32_t w = 0;
-            float s = 0.0f;
-            if (r < (side ? N : M)) {
-                w = __ldg(reinterpret_cast<const uint32_t*>((side ? b : a) + r * (K / 2) + blk * 16) + part);
-                s = e8m0_to_f32(__ldg((side ? bs : as) + r * (K / kMxBlock) + blk));
-            }
+            for (int i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const uint32_t*>(at) + i);
+        } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float2 p = e2m1x2_to_f32((w >> (8 * q)) & 0xFFu);
-                (side ? tb : ta)[part * 8 + 2 * q][row] = p.x * s;
-                (side ? tb : ta)[part * 8 + 2 * q + 1][row] = p.y * s;
+            for (int i = 0; i < 16; ++i) v[i >> 2] |= (i < n ? static_cast<uint32_t>(__ldg(at + i)) : 0u) << (8 * (i & 3));
+        }
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+template <int NT, int kType>
+__global__ void __launch_bounds__(256) k_few(const uint8_t* __restrict__ a, const uint8_t* __restrict__ as,
+                                             const uint8_t* __restrict__ b, const uint8_t* __restrict__ bs, int M, int64_t N, int K,
+                                             void* __restrict__ out) {
+    __shared__ float red[8][NT * 4][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int blocks = K / kMxBlock;
+    const uint8_t* rows[2] = {n0 + g < N ? b + (n0 + g) * (K / 2) : nullptr, n0 + g + 8 < N ? b + (n0 + g + 8) * (K / 2) : nullptr};
+    float acc[NT][4] = {};
+    for (int b0 = warp * 16; b0 < blocks; b0 += 8 * 16) {
+        uint32_t w[2][16], x[NT][16];
+        uint4 sw[2], sx[NT][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                w[i][j] = rows[i] && b0 + j < blocks ? __ldg(reinterpret_cast<const uint32_t*>(rows[i] + (b0 + j) * 16) + t) : 0u;
+            sw[i] = scales16(rows[i] ? bs + (n0 + g + 8 * i) * blocks : nullptr, b0, blocks);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int m = 8 * n + g;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                x[n][j] = m < M && b0 + j < blocks ? __ldg(reinterpret_cast<const uint32_t*>(a + (int64_t)m * (K / 2) + (b0 + j) * 16) + t) : 0u;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int mc = 8 * n + 2 * t + c;
+                sx[n][c] = scales16(mc < M ? as + (int64_t)mc * blocks : nullptr, b0, blocks);
             }
         }
-        __syncthreads();
-#pragma unroll 4
-        for (int k = 0; k < kMxBlock; ++k) {
-            float x[4], y[4];
+        auto word = [](const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
 #pragma unroll
-            for (int i = 0; i < 4; ++i) { x[i] = ta[k][tm + 16 * i]; y[i] = tb[k][tn + 16 * i]; }
+        for (int j4 = 0; j4 < 4; ++j4) {
+            float fw[2][4], fx[NT][2][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i) e8m0x4_to_f32(word(sw[i], j4), fw[i]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) e8m0x4_to_f32(word(sx[n][c], j4), fx[n][c]);
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+                const int j = 4 * j4 + jj;
+                uint32_t r0[4], r1[4];
+                e2m1x8_to_f16(w[0][j], r0);
+                e2m1x8_to_f16(w[1][j], r1);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    uint32_t c[4];
+                    e2m1x8_to_f16(x[n][j], c);
+                    float p[4];
+                    mma_f16(p, r0[0], r1[0], r0[1], r1[1], c[0], c[1], 0.0f, 0.0f, 0.0f, 0.0f);
+                    mma_f16(p, r0[2], r1[2], r0[3], r1[3], c[2], c[3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t u = __float_as_uint(fw[i >> 1][jj]), v = __float_as_uint(fx[n][i & 1][jj]);
+                        acc[n][i] = fmaf(p[i] * __uint_as_float(min(u, v)), __uint_as_float(max(u, v)), acc[n][i]);
+                    }
+                }
+            }
         }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + tm + 16 * i, n = n0 + tn + 16 * j;
-            if (m >= M || n >= N) continue;
-            if constexpr (kType == MOE_F32) static_cast<float*>(out)[m * N + n] = acc[i][j];
-            else static_cast<uint16_t*>(out)[m * N + n] = f32_to_bf16_bits(acc[i][j]);
-        }
+        for (int i = 0; i < 4; ++i) red[warp][n * 4 + i][lane] = acc[n][i];
+    __syncthreads();
+    for (int s = threadIdx.x; s < NT * 128; s += 256) {
+        const int i = s >> 5, m = (i >> 2) * 8 + 2 * t + (i & 1);
+        const int64_t n = n0 + g + 8 * ((i >> 1) & 1);
+        if (m >= M || n >= N) continue;
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) sum += red[w][i][lane];
+        if constexpr (kType == MOE_F32) static_cast<float*>(out)[m * N + n] = sum;
+        else static_cast<uint16_t*>(out)[m * N + n] = f32_to_bf16_bits(sum);
+    }
 }
+
+}  // namespace mxmm
 
 // ---- M > 16: tcgen05 -------------------------------------------------------------------------------
 //
@@ -111,24 +174,6 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
     d |= static_cast<uint64_t>(128 >> 4) << 32;
     d |= static_cast<uint64_t>(1) << 46;          // descriptor version (sm100), no swizzle
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
-}
-
-// Sixteen scales (blocks b .. b + 15) of a row of `blocks`; 0 past its end.  One 16-byte load where rows are
-// multiples of 16 blocks: loads of many rows cost their sectors, and this halves or quarters them.
-__device__ __forceinline__ uint4 scales16(const uint8_t* row, int b, int blocks) {
-    if (row == nullptr || b >= blocks) return make_uint4(0u, 0u, 0u, 0u);
-    if ((blocks & 15) == 0) return __ldg(reinterpret_cast<const uint4*>(row + b));
-    uint32_t v[4] = {0u, 0u, 0u, 0u};
-    if ((blocks & 3) == 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (b + 4 * i < blocks) v[i] = __ldg(reinterpret_cast<const uint32_t*>(row + b) + i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4 && b + 4 * i + j < blocks; ++j) v[i] |= static_cast<uint32_t>(__ldg(row + b + 4 * i + j)) << (8 * j);
-    }
-    return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 template <int BN, int kType>
@@ -362,11 +407,10 @@ extern "C" int mxfp4_matmul(const uint8_t* a, const uint8_t* a_scales, const uin
         return bn == 256 ? MOE_MM(256, MOE_BF16) : bn == 128 ? MOE_MM(128, MOE_BF16) : MOE_MM(64, MOE_BF16);
 #undef MOE_MM
     }
-    const dim3 grid(static_cast<unsigned>((N + 63) / 64), static_cast<unsigned>((M + 63) / 64));
-    if (grid.y > 65535) return MOE_ERR_UNSUPPORTED_SHAPE;
-    if (out_type == MOE_F32)
-        k_mxfp4_matmul<MOE_F32><<<grid, 256, 0, stream>>>(a, a_scales, b, b_scales, M, N, (int)K, out);
-    else
-        k_mxfp4_matmul<MOE_BF16><<<grid, 256, 0, stream>>>(a, a_scales, b, b_scales, M, N, (int)K, out);
+    const unsigned grid = static_cast<unsigned>((N + 15) / 16);
+#define MOE_MF(NT, TYPE) mxmm::k_few<NT, TYPE><<<grid, 256, 0, stream>>>(a, a_scales, b, b_scales, (int)M, N, (int)K, out)
+    if (out_type == MOE_F32) { if (M <= 8) MOE_MF(1, MOE_F32); else MOE_MF(2, MOE_F32); }
+    else { if (M <= 8) MOE_MF(1, MOE_BF16); else MOE_MF(2, MOE_BF16); }
+#undef MOE_MF
     return launch_status();
 }

@@ -135,13 +135,15 @@ def quant_mxfp4(x, stream=None):
     """bf16, f16 or fp32 values [..., K] on the GPU -> (E2M1 codes uint8 [..., K/2], E8M0 scales
     uint8 [..., K/32]).  Two-dimensional x may have strided rows."""
     import torch
-    *lead, K = x.shape
+    if x.dim() != 2:
+        codes, scales = quant_mxfp4(x.reshape(-1, x.shape[-1]), stream=stream)
+        return codes.view(*x.shape[:-1], -1), scales.view(*x.shape[:-1], -1)
+    rows, K = x.shape
     if K % 32:
         raise ValueError("K must be a multiple of 32")
-    rows = x if x.dim() == 2 else x.reshape(-1, K)
-    codes = torch.empty(*lead, K // 2, dtype=torch.uint8, device=x.device)
-    scales = torch.empty(*lead, K // 32, dtype=torch.uint8, device=x.device)
-    mxfp4_quant_rows(rows, codes.view(-1, K // 2), scales.view(-1, K // 32), stream=stream)
+    codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((rows, K // 32), dtype=torch.uint8, device=x.device)
+    mxfp4_quant_rows(x, codes, scales, stream=stream)
     return codes, scales
 
 
@@ -149,9 +151,11 @@ def dequant_mxfp4(codes, scales, dtype=None, stream=None):
     """The values [..., K] of MXFP4 codes [..., K/2] and scales [..., K/32], bf16 (the default) or
     fp32, both exact."""
     import torch
-    *lead, half = codes.shape
-    y = torch.empty(*lead, 2 * half, dtype=dtype or torch.bfloat16, device=codes.device)
-    mxfp4_dequant_rows(codes.view(-1, half), scales.view(-1, half // 16), y.view(-1, 2 * half), stream=stream)
+    if codes.dim() != 2:
+        y = dequant_mxfp4(codes.reshape(-1, codes.shape[-1]), scales.reshape(-1, scales.shape[-1]), dtype, stream=stream)
+        return y.view(*codes.shape[:-1], -1)
+    y = torch.empty((codes.shape[0], 2 * codes.shape[1]), dtype=dtype or torch.bfloat16, device=codes.device)
+    mxfp4_dequant_rows(codes, scales, y, stream=stream)
     return y
 
 

@@ -92,61 +92,88 @@ __device__ __forceinline__ void load8(const void* row, int64_t c, float (&f)[8])
     }
 }
 
-// Chunks of eight values, numbered through the rows (K / 8 a row); row_bytes apart in x.
-template <int kType>
+// Chunks of eight values, numbered through the rows (K / 8 a row), kMxUnroll a thread (256 apart, their loads all in
+// flight before the first is used).  kFlat: the rows follow one another, so a chunk's number is its address.
+constexpr int kMxUnroll = 4;
+
+template <int kType, bool kFlat>
 __global__ void __launch_bounds__(256) k_mxfp4_quant(const uint8_t* __restrict__ x, int64_t chunks, int per_row,
                                                       int64_t row_bytes, uint32_t* __restrict__ codes,
                                                       uint8_t* __restrict__ scales) {
-    const int64_t c = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-    const bool live = c < chunks;   // the four lanes of a block are live together
-    float f[8] = {};
-    if (live) {
-        const int64_t r = c / per_row;
-        load8<kType>(x + r * row_bytes, c - r * per_row, f);
-    }
-    uint32_t m = 0;
+    const int64_t c0 = blockIdx.x * (int64_t)(256 * kMxUnroll) + threadIdx.x;
+    float f[kMxUnroll][8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(f[q]) & 0x7FFFFFFFu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    if (!live) return;
-    const uint32_t field = m >> 23;   // of the block's maximum: floor(log2) + 127; 255: not finite
-    const uint32_t b = field == 255u ? 255u : field > 2u ? field - 2u : 0u;
-    uint32_t w = 0;
-    if (b != 255u) {
-        const float inv = __uint_as_float((254u - b) << 23);
+    for (int u = 0; u < kMxUnroll; ++u) {
+        const int64_t c = c0 + 256 * u;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) w |= f32x2_to_e2m1x2(f[2 * q] * inv, f[2 * q + 1] * inv) << (8 * q);
+        for (int q = 0; q < 8; ++q) f[u][q] = 0.0f;
+        if (c < chunks) {   // the four lanes of a block are live together
+            if constexpr (kFlat) {
+                load8<kType>(x, c, f[u]);
+            } else {
+                const int64_t r = c / per_row;
+                load8<kType>(x + r * row_bytes, c - r * per_row, f[u]);
+            }
+        }
     }
-    codes[c] = w;
-    if ((c & 3) == 0) scales[c >> 2] = static_cast<uint8_t>(b);
+#pragma unroll
+    for (int u = 0; u < kMxUnroll; ++u) {
+        const int64_t c = c0 + 256 * u;
+        uint32_t m = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(f[u][q]) & 0x7FFFFFFFu);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const uint32_t field = m >> 23;   // of the block's maximum: floor(log2) + 127; 255: not finite
+        const uint32_t b = field == 255u ? 255u : field > 2u ? field - 2u : 0u;
+        uint32_t w = 0;
+        if (b != 255u) {
+            const float inv = __uint_as_float((254u - b) << 23);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w |= f32x2_to_e2m1x2(f[u][2 * q] * inv, f[u][2 * q + 1] * inv) << (8 * q);
+        }
+        if (c < chunks) {
+            codes[c] = w;
+            if ((c & 3) == 0) scales[c >> 2] = static_cast<uint8_t>(b);
+        }
+    }
 }
 
 template <int kType>
 __global__ void __launch_bounds__(256) k_mxfp4_dequant(const uint32_t* __restrict__ codes,
                                                         const uint8_t* __restrict__ scales, int64_t chunks,
                                                         void* __restrict__ y) {
-    const int64_t c = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-    if (c >= chunks) return;
-    const uint32_t w = __ldg(codes + c);
-    const float s = e8m0_to_f32(__ldg(scales + (c >> 2)));
-    float f[8];
+    const int64_t c0 = blockIdx.x * (int64_t)(256 * kMxUnroll) + threadIdx.x;
+    uint32_t w[kMxUnroll], b[kMxUnroll];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const float2 p = e2m1x2_to_f32((w >> (8 * q)) & 0xFFu);
-        f[2 * q] = p.x * s;
-        f[2 * q + 1] = p.y * s;
+    for (int u = 0; u < kMxUnroll; ++u) {
+        const int64_t c = c0 + 256 * u;
+        w[u] = c < chunks ? __ldg(codes + c) : 0u;
+        b[u] = c < chunks ? __ldg(scales + (c >> 2)) : 0u;
     }
-    if constexpr (kType == MOE_F32) {
-        reinterpret_cast<float4*>(y)[2 * c] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4*>(y)[2 * c + 1] = make_float4(f[4], f[5], f[6], f[7]);
-    } else {
-        uint32_t o[4];   // exact: two significant bits, and bf16 has fp32's exponents
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            o[q] = static_cast<uint32_t>(f32_to_bf16_bits(f[2 * q])) |
-                   (static_cast<uint32_t>(f32_to_bf16_bits(f[2 * q + 1])) << 16);
-        reinterpret_cast<uint4*>(y)[c] = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int u = 0; u < kMxUnroll; ++u) {
+        const int64_t c = c0 + 256 * u;
+        if (c >= chunks) break;
+        const float s = e8m0_to_f32(b[u]);
+        float f[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float2 p = e2m1x2_to_f32((w[u] >> (8 * q)) & 0xFFu);
+            f[2 * q] = p.x * s;
+            f[2 * q + 1] = p.y * s;
+        }
+        if constexpr (kType == MOE_F32) {
+            reinterpret_cast<float4*>(y)[2 * c] = make_float4(f[0], f[1], f[2], f[3]);
+            reinterpret_cast<float4*>(y)[2 * c + 1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+            uint32_t o[4];   // exact: two significant bits, and bf16 has fp32's exponents
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                o[q] = static_cast<uint32_t>(f32_to_bf16_bits(f[2 * q])) |
+                       (static_cast<uint32_t>(f32_to_bf16_bits(f[2 * q + 1])) << 16);
+            reinterpret_cast<uint4*>(y)[c] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
     }
 }
 
@@ -170,16 +197,17 @@ extern "C" int mxfp4_quant_rows(const void* x, int x_type, int64_t rows, int64_t
     const int64_t row_bytes = (rows > 1 ? row_stride : K) * (x_type == MOE_F32 ? 4 : 2);
     if (!aligned(x, 16) || row_bytes % 16 != 0 || !aligned(codes, 4)) return MOE_ERR_MISALIGNED;
     const int64_t chunks = rows * (K / 8);
-    const unsigned grid = static_cast<unsigned>((chunks + 255) / 256);
+    const unsigned grid = static_cast<unsigned>((chunks + 256 * kMxUnroll - 1) / (256 * kMxUnroll));
     const uint8_t* xb = static_cast<const uint8_t*>(x);
     uint32_t* cw = reinterpret_cast<uint32_t*>(codes);
     const int per_row = static_cast<int>(K / 8);
-    if (x_type == MOE_BF16)
-        k_mxfp4_quant<MOE_BF16><<<grid, 256, 0, stream>>>(xb, chunks, per_row, row_bytes, cw, scales);
-    else if (x_type == MOE_F16)
-        k_mxfp4_quant<MOE_F16><<<grid, 256, 0, stream>>>(xb, chunks, per_row, row_bytes, cw, scales);
-    else
-        k_mxfp4_quant<MOE_F32><<<grid, 256, 0, stream>>>(xb, chunks, per_row, row_bytes, cw, scales);
+    const bool flat = row_bytes == K * (x_type == MOE_F32 ? 4 : 2);
+#define MOE_MQ(TYPE) (flat ? k_mxfp4_quant<TYPE, true><<<grid, 256, 0, stream>>>(xb, chunks, per_row, row_bytes, cw, scales) \
+                           : k_mxfp4_quant<TYPE, false><<<grid, 256, 0, stream>>>(xb, chunks, per_row, row_bytes, cw, scales))
+    if (x_type == MOE_BF16) MOE_MQ(MOE_BF16);
+    else if (x_type == MOE_F16) MOE_MQ(MOE_F16);
+    else MOE_MQ(MOE_F32);
+#undef MOE_MQ
     return launch_status();
 }
 
@@ -193,7 +221,7 @@ extern "C" int mxfp4_dequant_rows(const uint8_t* codes, const uint8_t* scales, i
     if (!codes || !scales || !y) return MOE_ERR_INVALID_ARG;
     if (!aligned(codes, 4) || !aligned(y, 16)) return MOE_ERR_MISALIGNED;
     const int64_t chunks = rows * (K / 8);
-    const unsigned grid = static_cast<unsigned>((chunks + 255) / 256);
+    const unsigned grid = static_cast<unsigned>((chunks + 256 * kMxUnroll - 1) / (256 * kMxUnroll));
     const uint32_t* cw = reinterpret_cast<const uint32_t*>(codes);
     if (y_type == MOE_BF16)
         k_mxfp4_dequant<MOE_BF16><<<grid, 256, 0, stream>>>(cw, scales, chunks, y);

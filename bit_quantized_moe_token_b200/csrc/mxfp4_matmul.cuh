@@ -145,13 +145,14 @@ constexpr int kStageK = 256;
 
 template <int BN>
 struct Cfg {
-    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 5 : 7;
+    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
     static constexpr int kA = 128 * 128, kB = BN * 128;
     static constexpr int kHalves = BN > 128 ? 2 : 1;                 // 128-row blocks of B's scales
-    static constexpr int kStage = kA + kB + 3072;                    // codes, then 1 KB of A's scales and up to 2 KB of B's
-    static constexpr int kSmem = 1024 + kStages * kStage + 8 * 2048;   // and the draining warps' buffers
+    static constexpr int kStage = kA + kB;
+    static constexpr int kCols = 4 * (2 + 2 * kHalves);              // TMEM columns of a stage's scales: A's 2 x 4, B's 2 x 4 kHalves
+    static constexpr int kSmem = 1024 + kStages * kStage + 8 * 2048 + 4 * 3072;   // and the draining and the scale warps' buffers
 };
-constexpr uint32_t kScaleColA = 256, kScaleColB = 264;               // TMEM columns: 2 x 4, 2 x 4 kHalves
+constexpr uint32_t kScaleCol = 256;                                  // the first of them
 
 __device__ __forceinline__ uint32_t idesc(int n, int sf) {
     return (static_cast<uint32_t>(sf) << 4)       // which of a column's four scales: B
@@ -167,13 +168,20 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
         ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)
         : "memory");
 }
-// 32 rows x 16 bytes of shared memory (512 contiguous bytes) -> four TMEM columns, in all four lane quadrants.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
-    uint64_t d = (saddr >> 4) & 0x3FFF;
-    d |= static_cast<uint64_t>(128 >> 4) << 16;   // core matrices (8 rows x 16 bytes) 128 bytes apart
-    d |= static_cast<uint64_t>(128 >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;          // descriptor version (sm100), no swizzle
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+// Four TMEM columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint4& v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// A barrier of the four scale warps that also tells whether all of them are well: they leave together or not at all.
+__device__ __forceinline__ bool all_well(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"(static_cast<uint32_t>(ok)) : "memory");
+    return r != 0;
 }
 
 template <int BN, int kType>
@@ -236,20 +244,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
                     ok = ws::wait(&full[r.idx], r.phase, &abort) && ws::wait(&scaled[r.idx], r.phase, &abort);
                     if (!ok) break;
                     tc::tc_fence_after();
-                    const uint32_t a = base + r.idx * C::kStage, sf = a + C::kA + C::kB;
-#pragma unroll
-                    for (int kb = 0; kb < 2; ++kb) {
-                        copy_scales(tmem + kScaleColA + 4 * kb, sf + 512 * kb);
-#pragma unroll
-                        for (int h = 0; h < C::kHalves; ++h)
-                            copy_scales(tmem + kScaleColB + 4 * (kb * C::kHalves + h), sf + 1024 + 512 * (kb * C::kHalves + h));
-                    }
+                    const uint32_t a = base + r.idx * C::kStage, sf = tmem + kScaleCol + r.idx * C::kCols;
                     const uint64_t da = tc::sdesc_sw128(a), db = tc::sdesc_sw128(a + C::kA);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (s * kStageK + 64 * j >= K) break;
-                        mma(tmem, da + 2 * j, db + 2 * j, idesc(BN, 2 * (j & 1)), tmem + kScaleColA + 4 * (j >> 1),
-                            tmem + kScaleColB + 4 * C::kHalves * (j >> 1), s > 0 || j > 0);
+                        mma(tmem, da + 2 * j, db + 2 * j, idesc(BN, 2 * (j & 1)), sf + 4 * (j >> 1),
+                            sf + 8 + 4 * C::kHalves * (j >> 1), s > 0 || j > 0);
                     }
                     tc::mma_commit(&empty[r.idx]);
                 }
@@ -258,8 +259,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
         }
     } else if (warp >= 8) {
         const int w = warp - 8;
+        uint8_t* buf = raw + (base - tc::smem_u32(raw)) + C::kStages * C::kStage + 8 * 2048;   // two pairs of stages
         ws::Ring<C::kStages> r;
-        for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+        bool well = true;   // of all four warps
+        uint32_t turn = 0;
+        for (int tile = blockIdx.x; well && tile < tiles; tile += gridDim.x) {
             const int m = tile / tn * 128 + 32 * w + lane, n = tile % tn * BN + 32 * w + lane;
             const uint8_t* rows[1 + C::kHalves];
             rows[0] = m < M ? as + (int64_t)m * blocks : nullptr;
@@ -273,25 +277,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
             };
 #pragma unroll
             for (int d = 0; d < kAhead; ++d) load(d, v[d]);
-            for (int s0 = 0; ok && s0 < stages; s0 += 2 * kAhead) {
+            for (int s0 = 0; well && s0 < stages; s0 += 2 * kAhead) {
 #pragma unroll
-                for (int d = 0; d < 2 * kAhead; ++d) {
-                    const int s = s0 + d;
-                    if (s >= stages || !(ok = ws::wait(&empty[r.idx], r.phase ^ 1u, &abort))) break;
-                    uint8_t* sf = raw + (base - tc::smem_u32(raw)) + r.idx * C::kStage + C::kA + C::kB + lane * 16 + w * 4;
+                for (int d = 0; d < kAhead; ++d) {
+                    if (!well || s0 + 2 * d >= stages) break;
+                    uint8_t* of = buf + (turn & 1u) * 6144 + lane * 16;
+                    ++turn;
 #pragma unroll
-                    for (int kb = 0; kb < 2; ++kb)
+                    for (int i = 0; i < 1 + C::kHalves; ++i) {
+                        uint8_t* to = of + w * 4 + 2048 * i;
+                        *reinterpret_cast<uint32_t*>(to) = v[d][i].x;
+                        *reinterpret_cast<uint32_t*>(to + 512) = v[d][i].y;
+                        *reinterpret_cast<uint32_t*>(to + 1024) = v[d][i].z;
+                        *reinterpret_cast<uint32_t*>(to + 1536) = v[d][i].w;
+                    }
+                    if (!(well = all_well(ok))) break;
+                    load(s0 / 2 + d + kAhead, v[d]);
+                    for (int s = s0 + 2 * d; ok && s < min(s0 + 2 * d + 2, stages); ++s, r.next()) {
+                        if (!(ok = __all_sync(~0u, ws::wait(&empty[r.idx], r.phase ^ 1u, &abort)))) break;
+                        tc::tc_fence_after();
+                        const uint32_t to = tmem + (static_cast<uint32_t>(w * 32) << 16) + kScaleCol + r.idx * C::kCols;
+                        const uint8_t* from = of + (s & 1) * 1024;
 #pragma unroll
-                        for (int i = 0; i < 1 + C::kHalves; ++i) {
-                            const uint4& q = v[d >> 1][i];
-                            *reinterpret_cast<uint32_t*>(sf + (i ? 1024 + 512 * (kb * C::kHalves + i - 1) : 512 * kb)) =
-                                d & 1 ? (kb ? q.w : q.z) : (kb ? q.y : q.x);
-                        }
-                    tc::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&scaled[r.idx]);
-                    if (d & 1) load(s / 2 + kAhead, v[d >> 1]);
-                    r.next();
+                        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                            for (int i = 0; i < 1 + C::kHalves; ++i)
+                                tmem_st4(to + (i ? 8 + 4 * (kb * C::kHalves + i - 1) : 4 * kb), *reinterpret_cast<const uint4*>(from + 2048 * i + 512 * kb));
+                        tc::tmem_wait_st();
+                        tc::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&scaled[r.idx]);
+                    }
                 }
             }
         }
@@ -300,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
         const int q = warp & 3, c0 = (warp >> 2) * kCols;
         uint32_t phase = 0;
         for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, phase ^= 1u) {
-            if (!(ok = ws::wait(&acc_full, phase, &abort))) break;
+            if (!(ok = __all_sync(~0u, ws::wait(&acc_full, phase, &abort)))) break;
             tc::tc_fence_after();
             uint32_t v[kType == MOE_F32 ? kCols : kCols / 2];
 #pragma unroll

@@ -143,10 +143,11 @@ namespace mxmm {
 constexpr int kThreads = 14 * 32;
 constexpr int kStageK = 256;
 
-template <int BN>
+template <int BN, bool kPair>
 struct Cfg {
-    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-    static constexpr int kA = 128 * 128, kB = BN * 128;
+    static constexpr int kStages = kPair ? 6 : BN == 256 ? 4 : BN == 128 ? 6 : 8;
+    static constexpr int kBRows = kPair ? BN / 2 : BN;               // of B in this CTA's shared memory
+    static constexpr int kA = 128 * 128, kB = kBRows * 128;
     static constexpr int kHalves = BN > 128 ? 2 : 1;                 // 128-row blocks of B's scales
     static constexpr int kStage = kA + kB;
     static constexpr int kCols = 4 * (2 + 2 * kHalves);              // TMEM columns of a stage's scales: A's 2 x 4, B's 2 x 4 kHalves
@@ -154,19 +155,28 @@ struct Cfg {
 };
 constexpr uint32_t kScaleCol = 256;                                  // the first of them
 
-__device__ __forceinline__ uint32_t idesc(int n, int sf) {
+__device__ __forceinline__ uint32_t idesc(int m, int n, int sf) {
     return (static_cast<uint32_t>(sf) << 4)       // which of a column's four scales: B
            | (1u << 7) | (1u << 10)               // A, B = E2M1
            | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23)   // N / 8, scales UE8M0
-           | (8u << 24) | (static_cast<uint32_t>(sf) << 29);      // M / 16, A's scales
+           | (static_cast<uint32_t>(m >> 4) << 24) | (static_cast<uint32_t>(sf) << 29);      // M / 16, A's scales
 }
+template <bool kPair>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t sa, uint32_t sb, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)
-        : "memory");
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)
+            : "memory");
 }
 // Four TMEM columns of this warp's 32 lanes.
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint4& v) {
@@ -184,37 +194,96 @@ __device__ __forceinline__ bool all_well(bool ok) {
     return r != 0;
 }
 
-template <int BN, int kType>
+// Arrives on `bar` (of both CTAs of a pair) once every MMA issued so far by this thread has completed.
+template <bool kPair>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    if constexpr (kPair)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(tc::smem_u32(bar)),
+                     "h"(static_cast<uint16_t>(3))
+                     : "memory");
+    else
+        tc::mma_commit(bar);
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot) {
+    if constexpr (kPair)
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_u32(slot)) : "memory");
+    else
+        tc::tmem_alloc(slot, 512);
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_free(uint32_t taddr) {
+    if constexpr (kPair) {
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(taddr) : "memory");
+    } else {
+        tc::tmem_relinquish();
+        tc::tmem_dealloc(taddr, 512);
+    }
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of `bar`'s place in the first CTA of the pair.
+__device__ __forceinline__ uint32_t in_first(uint64_t* bar) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(tc::smem_u32(bar)));
+    return a;
+}
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_first(bar)) : "memory");
+}
+// A TMA load into this CTA's shared memory whose bytes count on the first CTA's barrier.
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(tc::smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(in_first(bar))
+        : "memory");
+}
+
+template <int BN, int kType, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                                                       const uint8_t* __restrict__ as, const uint8_t* __restrict__ bs, int M, int N, int K,
                                                       void* __restrict__ out) {
-    using C = Cfg<BN>;
+    using C = Cfg<BN, kPair>;
+    constexpr int kRows = kPair ? 256 : 128;   // of A in a tile
     extern __shared__ __align__(16) uint8_t raw[];
     __shared__ uint64_t full[C::kStages], scaled[C::kStages], empty[C::kStages], acc_full, acc_empty;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort;
     const uint32_t base = (tc::smem_u32(raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tn = (N + BN - 1) / BN, tiles = (M + 127) / 128 * tn, stages = (K + kStageK - 1) / kStageK, blocks = K / kMxBlock;
+    const int tn = (N + BN - 1) / BN, tiles = (M + kRows - 1) / kRows * tn, stages = (K + kStageK - 1) / kStageK, blocks = K / kMxBlock;
+
+    // A pair of CTAs computes one tile: each has its 128 rows of A and of the accumulator and half of B; the first
+    // issues the MMAs, and what it waits for arrives on its barriers.
+    const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;
+    const int tile0 = kPair ? blockIdx.x / 2 : blockIdx.x, tile_step = kPair ? gridDim.x / 2 : gridDim.x;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             tc::mbar_init(&full[i], 1);
-            tc::mbar_init(&scaled[i], 4);
+            tc::mbar_init(&scaled[i], kPair ? 8 : 4);
             tc::mbar_init(&empty[i], 1);
         }
         tc::mbar_init(&acc_full, 1);
-        tc::mbar_init(&acc_empty, 8);
+        tc::mbar_init(&acc_empty, kPair ? 16 : 8);
         tc::fence_mbar_init();
         abort = 0;
     }
-    if (warp == 0) tc::tmem_alloc(&tmem_slot, 512);
+    if (warp == 0) tmem_alloc<kPair>(&tmem_slot);
     if (warp == 12 && lane == 0) {
         ws::prefetch_map(&map_a);
         ws::prefetch_map(&map_b);
     }
     tc::tc_fence_before();
-    __syncthreads();
+    if constexpr (kPair) cluster_sync();
+    else __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = tmem_slot;
     bool ok = true;
@@ -222,22 +291,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
     if (warp == 12) {
         if (lane == 0) {
             ws::Ring<C::kStages> r;
-            for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-                const int m0 = tile / tn * 128, n0 = tile % tn * BN;
+            for (int tile = tile0; ok && tile < tiles; tile += tile_step) {
+                const int m0 = tile / tn * kRows + rank * 128, n0 = tile % tn * BN + rank * C::kBRows;
                 for (int s = 0; s < stages; ++s, r.next()) {
                     if (!(ok = ws::wait(&empty[r.idx], r.phase ^ 1u, &abort))) break;
-                    tc::mbar_arrive_expect_tx(&full[r.idx], C::kA + C::kB);
+                    if (rank == 0) tc::mbar_arrive_expect_tx(&full[r.idx], (kPair ? 2 : 1) * C::kStage);
                     uint8_t* dst = raw + (base - tc::smem_u32(raw)) + r.idx * C::kStage;
-                    ws::tma_load_2d(dst, &map_a, s * 128, m0, &full[r.idx]);
-                    ws::tma_load_2d(dst + C::kA, &map_b, s * 128, n0, &full[r.idx]);
+                    if constexpr (kPair) {
+                        tma_load_pair(dst, &map_a, s * 128, m0, &full[r.idx]);
+                        tma_load_pair(dst + C::kA, &map_b, s * 128, n0, &full[r.idx]);
+                    } else {
+                        ws::tma_load_2d(dst, &map_a, s * 128, m0, &full[r.idx]);
+                        ws::tma_load_2d(dst + C::kA, &map_b, s * 128, n0, &full[r.idx]);
+                    }
                 }
             }
         }
     } else if (warp == 13) {
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             ws::Ring<C::kStages> r;
             uint32_t phase = 0;
-            for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, phase ^= 1u) {
+            for (int tile = tile0; ok && tile < tiles; tile += tile_step, phase ^= 1u) {
                 ok = ws::wait(&acc_empty, phase ^ 1u, &abort);
                 tc::tc_fence_after();
                 for (int s = 0; ok && s < stages; ++s, r.next()) {
@@ -249,12 +323,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (s * kStageK + 64 * j >= K) break;
-                        mma(tmem, da + 2 * j, db + 2 * j, idesc(BN, 2 * (j & 1)), sf + 4 * (j >> 1),
+                        mma<kPair>(tmem, da + 2 * j, db + 2 * j, idesc(kRows, BN, 2 * (j & 1)), sf + 4 * (j >> 1),
                             sf + 8 + 4 * C::kHalves * (j >> 1), s > 0 || j > 0);
                     }
-                    tc::mma_commit(&empty[r.idx]);
+                    commit<kPair>(&empty[r.idx]);
                 }
-                if (ok) tc::mma_commit(&acc_full);
+                if (ok) commit<kPair>(&acc_full);
             }
         }
     } else if (warp >= 8) {
@@ -263,8 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
         ws::Ring<C::kStages> r;
         bool well = true;   // of all four warps
         uint32_t turn = 0;
-        for (int tile = blockIdx.x; well && tile < tiles; tile += gridDim.x) {
-            const int m = tile / tn * 128 + 32 * w + lane, n = tile % tn * BN + 32 * w + lane;
+        for (int tile = tile0; well && tile < tiles; tile += tile_step) {
+            const int m = tile / tn * kRows + rank * 128 + 32 * w + lane, n = tile % tn * BN + 32 * w + lane;
             const uint8_t* rows[1 + C::kHalves];
             rows[0] = m < M ? as + (int64_t)m * blocks : nullptr;
 #pragma unroll
@@ -306,7 +380,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
                         tc::tmem_wait_st();
                         tc::tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&scaled[r.idx]);
+                        if (lane == 0) {
+                            if constexpr (kPair) arrive_first(&scaled[r.idx]);
+                            else tc::mbar_arrive(&scaled[r.idx]);
+                        }
                     }
                 }
             }
@@ -315,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
         constexpr int kCols = BN / 2;
         const int q = warp & 3, c0 = (warp >> 2) * kCols;
         uint32_t phase = 0;
-        for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, phase ^= 1u) {
+        for (int tile = tile0; ok && tile < tiles; tile += tile_step, phase ^= 1u) {
             if (!(ok = __all_sync(~0u, ws::wait(&acc_full, phase, &abort)))) break;
             tc::tc_fence_after();
             uint32_t v[kType == MOE_F32 ? kCols : kCols / 2];
@@ -334,8 +411,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
             }
             tc::tc_fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&acc_empty);
-            const int m0 = tile / tn * 128 + q * 32, n0 = tile % tn * BN + c0;
+            if (lane == 0) {
+                if constexpr (kPair) arrive_first(&acc_empty);
+                else tc::mbar_arrive(&acc_empty);
+            }
+            const int m0 = tile / tn * kRows + rank * 128 + q * 32, n0 = tile % tn * BN + c0;
             constexpr int kElem = kType == MOE_F32 ? 4 : 2, kVec = 16 / kElem;
             if (N % kVec == 0) {
                 // 64 bytes of each of the 32 rows at a time through shared memory, so that a store writes whole rows'
@@ -376,24 +456,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
         const uint64_t t0 = tc::globaltimer_ns();
         while (tc::globaltimer_ns() - t0 < 10000000ull) __nanosleep(100000);
     }
+    if constexpr (kPair) cluster_sync();   // neither leaves while the other may still use its barriers or memory
     tc::tc_fence_after();
-    if (warp == 0) {
-        tc::tmem_relinquish();
-        tc::tmem_dealloc(tmem, 512);
-    }
+    if (warp == 0) tmem_free<kPair>(tmem);
 }
 
-template <int BN, int kType>
+template <int BN, int kType, bool kPair = false>
 inline int launch(const uint8_t* a, const uint8_t* as, const uint8_t* b, const uint8_t* bs, int M, int N, int K, void* out, int sms,
                   cudaStream_t stream) {
+    using C = Cfg<BN, kPair>;
     CUtensorMap ma, mb;
     if (!make_map_u8(&ma, a, K / 2, M, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map_u8(&mb, b, K / 2, N, 128, BN, CU_TENSOR_MAP_SWIZZLE_128B))
+        !make_map_u8(&mb, b, K / 2, N, 128, C::kBRows, CU_TENSOR_MAP_SWIZZLE_128B))
         return MOE_ERR_CUDA;
-    if (set_smem(reinterpret_cast<const void*>(k_gemm<BN, kType>), Cfg<BN>::kSmem)) return MOE_ERR_CUDA;
-    const int64_t tiles = (int64_t)((M + 127) / 128) * ((N + BN - 1) / BN);
-    k_gemm<BN, kType><<<static_cast<unsigned>(std::min<int64_t>(tiles, sms)), kThreads, Cfg<BN>::kSmem, stream>>>(ma, mb, as, bs, M, N, K, out);
-    return launch_status();
+    const void* fn = reinterpret_cast<const void*>(k_gemm<BN, kType, kPair>);
+    if (set_smem(fn, C::kSmem)) return MOE_ERR_CUDA;
+    constexpr int kRows = kPair ? 256 : 128;
+    const int64_t tiles = (int64_t)((M + kRows - 1) / kRows) * ((N + BN - 1) / BN);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(kPair ? 2 * std::min<int64_t>(tiles, sms / 2) : std::min<int64_t>(tiles, sms)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kPair ? 2 : 1;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, k_gemm<BN, kType, kPair>, ma, mb, as, bs, M, N, K, out) == cudaSuccess) return MOE_OK;
+    (void)cudaGetLastError();   // a rejected launch leaves no error behind for later calls
+    return MOE_ERR_CUDA;
 }
 
 }  // namespace mxmm
@@ -415,12 +508,15 @@ extern "C" int mxfp4_matmul(const uint8_t* a, const uint8_t* a_scales, const uin
         if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return MOE_ERR_CUDA;
         const int m = (int)M, n = (int)N, k = (int)K;
-        // the widest tile that gives every SM one
+        // pairs of CTAs (256 x 256) where they fill the SMs, else the widest tile that gives every SM one
         const int64_t rows = (M + 127) / 128;
-        const int bn = rows * ((N + 255) / 256) >= sms ? 256 : rows * ((N + 127) / 128) >= sms ? 128 : 64;
+        if ((M + 255) / 256 * ((N + 255) / 256) >= sms / 2)
+            return out_type == MOE_F32 ? mxmm::launch<256, MOE_F32, true>(a, a_scales, b, b_scales, m, n, k, out, sms, stream)
+                                       : mxmm::launch<256, MOE_BF16, true>(a, a_scales, b, b_scales, m, n, k, out, sms, stream);
+        const int bn = rows * ((N + 127) / 128) >= sms ? 128 : 64;
 #define MOE_MM(BN, TYPE) mxmm::launch<BN, TYPE>(a, a_scales, b, b_scales, m, n, k, out, sms, stream)
-        if (out_type == MOE_F32) return bn == 256 ? MOE_MM(256, MOE_F32) : bn == 128 ? MOE_MM(128, MOE_F32) : MOE_MM(64, MOE_F32);
-        return bn == 256 ? MOE_MM(256, MOE_BF16) : bn == 128 ? MOE_MM(128, MOE_BF16) : MOE_MM(64, MOE_BF16);
+        if (out_type == MOE_F32) return bn == 128 ? MOE_MM(128, MOE_F32) : MOE_MM(64, MOE_F32);
+        return bn == 128 ? MOE_MM(128, MOE_BF16) : MOE_MM(64, MOE_BF16);
 #undef MOE_MM
     }
     const unsigned grid = static_cast<unsigned>((N + 15) / 16);

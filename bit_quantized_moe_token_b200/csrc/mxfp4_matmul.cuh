@@ -155,6 +155,16 @@ struct Cfg {
 };
 constexpr uint32_t kScaleCol = 256;                                  // the first of them
 
+// One lane of the warp, in a form that lets the compiler keep what that lane issues in uniform registers.
+__device__ __forceinline__ bool elected() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
 __device__ __forceinline__ uint32_t idesc(int m, int n, int sf) {
     return (static_cast<uint32_t>(sf) << 4)       // which of a column's four scales: B
            | (1u << 7) | (1u << 10)               // A, B = E2M1
@@ -253,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
     using C = Cfg<BN, kPair>;
     constexpr int kRows = kPair ? 256 : 128;   // of A in a tile
     extern __shared__ __align__(16) uint8_t raw[];
-    __shared__ uint64_t full[C::kStages], scaled[C::kStages], empty[C::kStages], acc_full, acc_empty;
+    __shared__ uint64_t full[C::kStages], empty[C::kStages], acc_full, acc_empty;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort;
     const uint32_t base = (tc::smem_u32(raw) + 1023u) & ~1023u;
@@ -267,8 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            tc::mbar_init(&full[i], 1);
-            tc::mbar_init(&scaled[i], kPair ? 8 : 4);
+            tc::mbar_init(&full[i], 1 + (kPair ? 8 : 4));   // the bytes, and the scale warps
             tc::mbar_init(&empty[i], 1);
         }
         tc::mbar_init(&acc_full, 1);
@@ -289,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
     bool ok = true;
 
     if (warp == 12) {
-        if (lane == 0) {
+        if (elected()) {
             ws::Ring<C::kStages> r;
             for (int tile = tile0; ok && tile < tiles; tile += tile_step) {
                 const int m0 = tile / tn * kRows + rank * 128, n0 = tile % tn * BN + rank * C::kBRows;
@@ -308,14 +317,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
             }
         }
     } else if (warp == 13) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0 && elected()) {
             ws::Ring<C::kStages> r;
             uint32_t phase = 0;
             for (int tile = tile0; ok && tile < tiles; tile += tile_step, phase ^= 1u) {
                 ok = ws::wait(&acc_empty, phase ^ 1u, &abort);
                 tc::tc_fence_after();
                 for (int s = 0; ok && s < stages; ++s, r.next()) {
-                    ok = ws::wait(&full[r.idx], r.phase, &abort) && ws::wait(&scaled[r.idx], r.phase, &abort);
+                    ok = ws::wait(&full[r.idx], r.phase, &abort);
                     if (!ok) break;
                     tc::tc_fence_after();
                     const uint32_t a = base + r.idx * C::kStage, sf = tmem + kScaleCol + r.idx * C::kCols;
@@ -381,8 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
                         tc::tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            if constexpr (kPair) arrive_first(&scaled[r.idx]);
-                            else tc::mbar_arrive(&scaled[r.idx]);
+                            if constexpr (kPair) arrive_first(&full[r.idx]);
+                            else tc::mbar_arrive(&full[r.idx]);
                         }
                     }
                 }

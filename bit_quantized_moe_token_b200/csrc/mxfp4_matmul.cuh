@@ -140,18 +140,19 @@ __global__ void __launch_bounds__(256) k_few(const uint8_t* __restrict__ a, cons
 // it, and store while the next tile's MMAs run.
 namespace mxmm {
 
-constexpr int kThreads = 14 * 32;
 constexpr int kStageK = 256;
 
 template <int BN, bool kPair>
 struct Cfg {
     static constexpr int kStages = kPair ? 6 : BN == 256 ? 4 : BN == 128 ? 6 : 8;
+    static constexpr int kDrain = BN == 256 ? 16 : 8;                // warps that drain the accumulator
+    static constexpr int kThreads = (kDrain + 6) * 32;
     static constexpr int kBRows = kPair ? BN / 2 : BN;               // of B in this CTA's shared memory
     static constexpr int kA = 128 * 128, kB = kBRows * 128;
     static constexpr int kHalves = BN > 128 ? 2 : 1;                 // 128-row blocks of B's scales
     static constexpr int kStage = kA + kB;
     static constexpr int kCols = 4 * (2 + 2 * kHalves);              // TMEM columns of a stage's scales: A's 2 x 4, B's 2 x 4 kHalves
-    static constexpr int kSmem = 1024 + kStages * kStage + 8 * 2048 + 4 * 3072;   // and the draining and the scale warps' buffers
+    static constexpr int kSmem = 1024 + kStages * kStage + kDrain * 1024 + 4 * 3072;   // and the draining and the scale warps' buffers
 };
 constexpr uint32_t kScaleCol = 256;                                  // the first of them
 
@@ -257,7 +258,7 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map,
 }
 
 template <int BN, int kType, bool kPair>
-__global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+__global__ void __launch_bounds__(Cfg<BN, kPair>::kThreads, 1) k_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                                                       const uint8_t* __restrict__ as, const uint8_t* __restrict__ bs, int M, int N, int K,
                                                       void* __restrict__ out) {
     using C = Cfg<BN, kPair>;
@@ -281,12 +282,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
             tc::mbar_init(&empty[i], 1);
         }
         tc::mbar_init(&acc_full, 1);
-        tc::mbar_init(&acc_empty, kPair ? 16 : 8);
+        tc::mbar_init(&acc_empty, (kPair ? 2 : 1) * C::kDrain);
         tc::fence_mbar_init();
         abort = 0;
     }
     if (warp == 0) tmem_alloc<kPair>(&tmem_slot);
-    if (warp == 12 && lane == 0) {
+    if (warp == C::kDrain + 4 && lane == 0) {
         ws::prefetch_map(&map_a);
         ws::prefetch_map(&map_b);
     }
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
     const uint32_t tmem = tmem_slot;
     bool ok = true;
 
-    if (warp == 12) {
+    if (warp == C::kDrain + 4) {
         if (elected()) {
             ws::Ring<C::kStages> r;
             for (int tile = tile0; ok && tile < tiles; tile += tile_step) {
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
                 }
             }
         }
-    } else if (warp == 13) {
+    } else if (warp == C::kDrain + 5) {
         if (rank == 0 && elected()) {
             ws::Ring<C::kStages> r;
             uint32_t phase = 0;
@@ -340,9 +341,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
                 if (ok) commit<kPair>(&acc_full);
             }
         }
-    } else if (warp >= 8) {
-        const int w = warp - 8;
-        uint8_t* buf = raw + (base - tc::smem_u32(raw)) + C::kStages * C::kStage + 8 * 2048;   // two pairs of stages
+    } else if (warp >= C::kDrain) {
+        const int w = warp - C::kDrain;
+        uint8_t* buf = raw + (base - tc::smem_u32(raw)) + C::kStages * C::kStage + C::kDrain * 1024;   // two pairs of stages
         ws::Ring<C::kStages> r;
         bool well = true;   // of all four warps
         uint32_t turn = 0;
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
             }
         }
     } else {
-        constexpr int kCols = BN / 2;
+        constexpr int kCols = BN / (C::kDrain / 4);
         const int q = warp & 3, c0 = (warp >> 2) * kCols;
         uint32_t phase = 0;
         for (int tile = tile0; ok && tile < tiles; tile += tile_step, phase ^= 1u) {
@@ -429,21 +430,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
             if (N % kVec == 0) {
                 // 64 bytes of each of the 32 rows at a time through shared memory, so that a store writes whole rows'
                 // segments (chunk c of row l at c ^ (l / 2) % 4: no bank conflicts either way)
-                uint8_t* buf = raw + (base - tc::smem_u32(raw)) + C::kStages * C::kStage + warp * 2048;
+                uint8_t* buf = raw + (base - tc::smem_u32(raw)) + C::kStages * C::kStage + warp * 1024;
 #pragma unroll
                 for (int c = 0; c < kCols * kElem / 64; ++c) {
-                    __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4*>(buf + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
-                            make_uint4(v[16 * c + 4 * i], v[16 * c + 4 * i + 1], v[16 * c + 4 * i + 2], v[16 * c + 4 * i + 3]);
-                    __syncwarp();
+                    for (int h = 0; h < 2; ++h) {   // 16 rows at a time
+                        __syncwarp();
+                        if (lane >> 4 == h) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = i * 8 + (lane >> 2), n = n0 + (64 / kElem) * c + (lane & 3) * kVec;
-                        const uint4 x = *reinterpret_cast<const uint4*>(buf + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
-                        if (m0 + row < M && n < N)
-                            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + ((int64_t)(m0 + row) * N + n) * kElem) = x;
+                            for (int i = 0; i < 4; ++i)
+                                *reinterpret_cast<uint4*>(buf + (lane & 15) * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+                                    make_uint4(v[16 * c + 4 * i], v[16 * c + 4 * i + 1], v[16 * c + 4 * i + 2], v[16 * c + 4 * i + 3]);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int row = i * 8 + (lane >> 2), m = m0 + 16 * h + row, n = n0 + (64 / kElem) * c + (lane & 3) * kVec;
+                            const uint4 x = *reinterpret_cast<const uint4*>(buf + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
+                            if (m < M && n < N) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + ((int64_t)m * N + n) * kElem) = x;
+                        }
                     }
                 }
             } else if (m0 + lane < M) {
@@ -484,7 +489,7 @@ inline int launch(const uint8_t* a, const uint8_t* as, const uint8_t* b, const u
     const int64_t tiles = (int64_t)((M + kRows - 1) / kRows) * ((N + BN - 1) / BN);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(kPair ? 2 * std::min<int64_t>(tiles, sms / 2) : std::min<int64_t>(tiles, sms)));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -31,6 +31,13 @@ __device__ __forceinline__ uint4 scales16(const uint8_t* row, int b, int blocks)
         if (n >= 16 && (low & 3u) == 0) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const uint32_t*>(at) + i);
+        } else if (n >= 20) {   // five whole words around them, all in this row and those before it
+            const uint32_t* words = reinterpret_cast<const uint32_t*>(at - (low & 3u));
+            uint32_t u[5];
+#pragma unroll
+            for (int i = 0; i < 5; ++i) u[i] = __ldg(words + i);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(u[i], u[i + 1], 8 * (low & 3u));
         } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i >> 2] |= (i < n ? static_cast<uint32_t>(__ldg(at + i)) : 0u) << (8 * (i & 3));
@@ -522,15 +529,17 @@ extern "C" int mxfp4_matmul(const uint8_t* a, const uint8_t* a_scales, const uin
         if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return MOE_ERR_CUDA;
         const int m = (int)M, n = (int)N, k = (int)K;
-        // pairs of CTAs (256 x 256) where they fill the SMs, else the widest tile that gives every SM one
-        const int64_t rows = (M + 127) / 128;
-        if ((M + 255) / 256 * ((N + 255) / 256) >= sms / 2)
+        // 64 columns a CTA while that is one wave (256 x 4096 x 4096: 9.8 us against 10.8 for 128).  Else 128, or 256 x 256
+        // for a pair of CTAs: a wave of the latter takes 1.5 times as long (11.3 us against 7.5 at K = 4096) for up to twice
+        // the outputs (512 rows x 4096: 11.0 us against 14.9; 1024: 19.0 against 15.9; 2048: 32.9 against 26.2).
+        const int64_t rows = (M + 127) / 128, t128 = rows * ((N + 127) / 128), t256 = (M + 255) / 256 * ((N + 255) / 256);
+        const bool narrow = rows * ((N + 63) / 64) <= sms;
+        if (!narrow && 3 * ((t256 + sms / 2 - 1) / (sms / 2)) <= 2 * ((t128 + sms - 1) / sms))
             return out_type == MOE_F32 ? mxmm::launch<256, MOE_F32, true>(a, a_scales, b, b_scales, m, n, k, out, sms, stream)
                                        : mxmm::launch<256, MOE_BF16, true>(a, a_scales, b, b_scales, m, n, k, out, sms, stream);
-        const int bn = rows * ((N + 127) / 128) >= sms ? 128 : 64;
 #define MOE_MM(BN, TYPE) mxmm::launch<BN, TYPE>(a, a_scales, b, b_scales, m, n, k, out, sms, stream)
-        if (out_type == MOE_F32) return bn == 128 ? MOE_MM(128, MOE_F32) : MOE_MM(64, MOE_F32);
-        return bn == 128 ? MOE_MM(128, MOE_BF16) : MOE_MM(64, MOE_BF16);
+        if (out_type == MOE_F32) return narrow ? MOE_MM(64, MOE_F32) : MOE_MM(128, MOE_F32);
+        return narrow ? MOE_MM(64, MOE_BF16) : MOE_MM(128, MOE_BF16);
 #undef MOE_MM
     }
     const unsigned grid = static_cast<unsigned>((N + 15) / 16);

@@ -5,41 +5,49 @@
 // SwiGLU), S5 (FP8 of h for each routed pair), S6 (down), S7 (the gated sum) and S8 (shared
 // experts), with the experts' weights in pack-quantized INT4 or in MXFP4.
 //
-// What bounds it: a few tokens use each weight once or twice, so the time is the reading of the
-// touched experts' weights (13 MB an expert at H = 4096, N = 2048) and, at one token, of launches.
-// So one persistent cooperative grid (one CTA an SM) streams every weight byte once through a ring
-// of shared-memory stages, and the stream does not stop at the layer's two inner dependencies: the
-// weights of the down projections do not depend on h, so the producer warp fills the whole ring
-// with them while the grid finishes h (barrier), quantizes it (barrier) and comes back to read.
+// What bounds it: a few tokens use each weight once or twice, so the time is the reading of the touched experts' weights
+// (13 MB an expert at H = 4096, N = 2048) and, at one token, a chain of latencies.  One persistent cooperative grid (one
+// CTA an SM) therefore reads every weight byte once, and the stream does not stop at the layer's inner dependency: the
+// weights of the down projections do not depend on h, so the rings fill with them while the grid finishes h.
 //
-//   prologue  every CTA ranks the logits itself (one warp a token), lists the touched experts and
-//             starts streaming; meanwhile the consumer warps quantize the tokens into shared memory
-//   phase A   unit = 8 gate rows and the same 8 up rows of one touched expert, all of K; the
-//             units are split evenly over the CTAs; h (fp32) goes to the workspace
-//   barrier, S5 (one CTA a routed pair), barrier
-//   phase B   unit = 16 down rows of one touched expert; units run tile by tile (16 outputs of every
-//             token), so a tile's experts add up in registers, in a fixed order; the two CTAs that
-//             share a tile at the border of their ranges leave partial sums, and the one that comes
-//             last adds them, again in a fixed order
+//   prologue  (router form: the logits, a barrier.)  Every CTA ranks the logits itself, a warp a token, lists the touched
+//             experts and starts streaming; meanwhile the multiplying warps quantize the tokens that its experts need into
+//             B fragments in shared memory: f16 for up to six tokens, FP8 (widened at each use) beyond: at T = 16 three
+//             experts' tokens seldom are more, and the widening would cost every piece
+//   gate/up   unit = 8 gate rows and the same 8 up rows of one touched expert, all of K; a phase's units are split evenly
+//             over the CTAs; h (fp32) goes to the workspace.  Then the shared experts' (bf16)
+//   barrier   each CTA quantizes the rows of h that its down units read into its own shared memory; where some CTA's rows
+//             do not fit, CTA r quantizes row r into the workspace and a second barrier follows (own rows: 41 us at T = 1
+//             against 44, the barrier)
+//   down      unit = 16 rows of one touched expert (then of a shared expert); gated rows to the workspace
+//   barrier   the rows are added in selection order
 //
-// A stage is 16 rows x 2 KB (32 KB): 16 pieces of 16 rows x 128 bytes, one for each consumer warp
-// (a row longer than 2 KB takes several stages, shorter rows put several units into one).  It is
-// loaded by one TMA box for each of its row sets, in the 128-byte swizzle, so a warp reads 16 bytes
-// of eight rows without bank conflicts.
+// Eight warps multiply and four stream for them.  A warp has rings of its own (two to four slots of 8 KB, chunks of 4
+// pieces of 16 rows x 128 bytes in the 128-byte swizzle, one TMA box a row set), so that no warp waits for another's data;
+// a streaming warp has a lane for each ring it feeds.  Issued by the multiplying warps themselves a chunk's copies cost
+// them some 1,000 cycles.  Other divisions, in us for W4A8 (T = 1, 8, 16) and MXFP4 (T = 1, 8):
+//   8 + 4 warps   38.6  138  288   41  138        12 + 4   36.9  146  336   40  146
+//   9 + 3         40.3  143  333   44  154        10 + 2   39.6  145  339   44  163
+// and the loop over a chunk's pieces unrolled twice (rolled it stays in the instruction cache): 40.1 144 300 43 142.
+// A row's scales come beside its unit's first chunk where the buffers fit, else they are read in place.
 //
-// The products run on mma.sync m16n8k16 (f16, fp32 sums): the rows are the M = 16, up to eight
-// tokens the N = 8.  tcgen05 would put 128 rows a tile and the widened weights through TMEM for the
-// same eight columns; here its rate is not needed (the stream leaves an SM 1,400 cycles a stage),
-// and a warp's registers hold the whole tile.  E4M3 values are exact in f16, and so are the weights:
-//   INT4:  a nibble n = code + 8 left where it lies in a 16-bit half is the f16 subnormal n 2^-24
-//          (bits 0..3) or n 2^-20 (bits 4..7, whose tokens' values carry 2^-4), so widening a packed
-//          word costs four ANDs and a shift; the accumulator starts at -8 2^-24 sum q, which takes
-//          the offset off again.
+// The products run on mma.sync m16n8k16 (f16, fp32 sums): a unit's 16 rows are the M, up to eight tokens the N.  tcgen05
+// would put 128 rows a tile, and the widened weights through TMEM, for the same eight columns.  E4M3 values are exact in
+// f16, and so are the weights:
+//   INT4:  a nibble n = code + 8 left where it lies in a 16-bit half is the f16 subnormal n 2^-24 (bits 0..3) or n 2^-20
+//          (bits 4..7, whose tokens' values carry 2^-4), so widening a packed word costs four ANDs and a shift; the
+//          accumulator starts at -8 2^-24 sum q, which takes the offset off again.
 //   MXFP4: cvt.rn.f16x2.e2m1x2.
-// (mma.sync on E4M3 is no way round the conversion: it took 400 warp instructions a stage and warp
-// against 190, and the layer at T = 8 took 213 us.)
-// A group's (block's) partial sum is scaled in fp32 by its weight scale: one promotion every 128
-// (32) weights.  Shared experts run on the bf16 MMA, their activation as bf16 hi + lo halves.
+// (mma.sync on E4M3 is no way round the conversion: with it the layer at T = 8 took 213 us.)  A group's (block's) partial
+// sum is scaled in fp32 by its weight scale: one promotion every 128 (32) weights.  Shared experts run on the bf16 MMA,
+// their activation as bf16 hi + lo halves (16 bits of it).
+//
+// Measured, E = 256, top 6, H = 4096, N = 2048: W4A8 T = 1 38.6 us (78 MB: 31 % of HBM's measured 6.56 TB/s), T = 8 with
+// the router 138 us (578 MB: 64 %), T = 16 with two shared experts 288 us (1.15 GB: 61 %); MXFP4 T = 1 with the router
+// 41 us, T = 8 138 us (593 MB: 65 %).  At T = 1 the chain is: lists 4.6 us, tokens quantized 9.5, gate/up 22.5, barrier
+// 24.8, h quantized 26.5, down 32.6, sums 35.  At T = 8 the same grid reads the bytes in 104 us when nothing is
+// multiplied; a warp needs some 640 cycles a piece (widening, fragments, MMAs, promotion), eight of them 80 cycles for
+// 2 KB, which is just the rate at which HBM delivers them.
 #pragma once
 #include <cooperative_groups.h>
 #include <type_traits>

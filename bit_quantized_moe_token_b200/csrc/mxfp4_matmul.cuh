@@ -7,7 +7,7 @@
 
 namespace moe {
 
-// ---- M <= 16: mma.sync ----------------------------------------------------------------------------
+// ---- M <= 16 and one wave: mma.sync ----------------------------------------------------------------------------
 //
 // A few tokens' product is the reading of B.  A CTA takes 16 rows of B (the MMA's M = 16; tokens are its N = 8
 // columns, in one or two blocks) and its eight warps 512 columns at a time each; a warp asks for all of its codes
@@ -16,7 +16,12 @@ namespace moe {
 // MMA pair covers one block; E2M1 is exact in f16.  A block's sum is a multiple of 1/4 below 2^11: multiplied first by
 // the smaller of its two scales it neither overflows (unless the result does) nor loses bits, and a scale of 255 (NaN,
 // the largest as bits too) stays what it is.
-// Tokens beyond 16 go to the tensor-memory kernel, which reads 128 rows of A whatever M is.
+// Measured (bf16 out): 4096 x 4096 weights at M = 1 6.2 us (8.9 MB: 22 % of HBM's measured rate, a chain of latencies), at
+// M = 8 7.7.  It serves one wave of CTAs, two an SM for up to eight tokens and one beyond; more rows of B, and M > 16, go
+// to the tensor-memory kernel, which reads 128 rows of A whatever M is.  This kernel against that one, in us:
+//   M = 1, 4096 x 4096  6.2 10.3    M = 8, 4096 x 4096  7.7 10.3    M = 16, 2048 x 4096  6.2  9.2
+//          8192 x 4096 10.8 12.4           8192 x 4096 13.4 12.4            4096 x 4096 11.3 10.5
+//         14336 x 4096 18.1 13.9          14336 x 4096 22.1 14.3           14336 x 4096 38.5 14.7
 namespace mxmm {
 
 // Sixteen scales (blocks b .. b + 15) of a row of `blocks`; 0 past its end.  One 16-byte load where the row allows it:
@@ -129,22 +134,32 @@ __global__ void __launch_bounds__(256) k_few(const uint8_t* __restrict__ a, cons
 
 }  // namespace mxmm
 
-// ---- M > 16: tcgen05 -------------------------------------------------------------------------------
+// ---- else: tcgen05 -------------------------------------------------------------------------------
 //
-// kind::mxf4.block_scale takes both operands as they are stored: 128 x BN outputs a CTA, K in stages of
-// 256 codes (128-byte rows, TMA in the 128-byte swizzle), four MMAs of K = 64 a stage into one fp32
-// accumulator in TMEM, each block's two scales applied by the tensor core (products exact, fp32 sums).
+// kind::mxf4.block_scale takes both operands as they are stored: K in stages of 256 codes (128-byte rows, TMA in the
+// 128-byte swizzle), four MMAs of K = 64 a stage into one fp32 accumulator in TMEM, each block's two scales applied by the
+// tensor core (products exact, fp32 sums).  A tile is 128 x BN outputs of a CTA, or 256 x 256 of a pair of CTAs
+// (cta_group::2): each has 128 rows of A and of the accumulator and half of B's rows, the first issues the MMAs.
 //
-// Roles: warps 0-7 drain the accumulator, 8-11 bring the scales, 12 issues the TMA loads, 13 the MMAs.
-// The scale warps read each row's eight E8M0 bytes of a stage from their rows (K / 32 bytes apart; no
-// TMA box is that narrow) and lay them out as the tensor core wants them: 512-byte blocks of 128 rows x
-// 4 scales, row r at (r % 32) 16 + (r / 32) 4, which tcgen05.cp (32x128b.warpx4) copies to four TMEM
-// columns.  The copies are issued by the MMA thread ahead of the stage's MMAs; both execute in order, so
-// one set of TMEM columns serves all stages.
+// Roles: kDrain warps drain the accumulator, four bring the scales, one thread issues the TMA loads, one the MMAs.
 //
-// The accumulator's BN = 256 columns and the scales leave no room in TMEM for a second accumulator, so
-// the eight draining warps first take it into registers (rounded to the output type: 64 registers), free
-// it, and store while the next tile's MMAs run.
+// Scales.  The tensor core wants 128 rows' four scales of 128 codes as four TMEM columns: row 32 c + l in lane l of
+// column c, the same in all four lane quadrants.  No TMA box is as narrow as a row's eight bytes a stage, so the scale
+// warps read 16 bytes a row (two stages) two such pairs ahead, exchange them through shared memory and each stores its
+// quadrant's columns with tcgen05.st.  (tcgen05.cp from shared memory, issued ahead of the stage's MMAs, held up the MMAs:
+// 16384 x 4096 x 4096 in 173 us against 156.)
+//
+// The issuing thread.  What it does a stage has to take less than the stage's 512 cycles of MMA: one barrier for the bytes
+// and the scales, and a thread chosen by elect.sync, whose operands the compiler keeps in uniform registers (with two
+// barriers and lane 0 a stage took it 980 cycles, 530 of them to issue; 147 us against 144).
+//
+// The accumulator's 256 columns and the scales leave no room in TMEM for a second one, so the draining warps first take it
+// into registers (rounded to the output type), free it, and store while the next tile's MMAs run: sixteen warps of 64
+// columns, whose registers suffice without spills (eight of 128: 144 us against 136).
+//
+// Measured (bf16 out): 16384 x 4096 x 4096 135 us = 4,070 TFLOP/s, 2.4 times the measured bf16 peak (FP4's nominal rate is
+// four times bf16's); K = 8192 4,490; 2048 x 4096 x 4096 24.3 us: two waves for 1.73 waves of tiles.  Without the drain's
+// stores the first takes 123 us, without MMAs for half of K 110: the rest is the fill and drain of each tile.
 namespace mxmm {
 
 constexpr int kStageK = 256;
@@ -159,7 +174,7 @@ struct Cfg {
     static constexpr int kHalves = BN > 128 ? 2 : 1;                 // 128-row blocks of B's scales
     static constexpr int kStage = kA + kB;
     static constexpr int kCols = 4 * (2 + 2 * kHalves);              // TMEM columns of a stage's scales: A's 2 x 4, B's 2 x 4 kHalves
-    static constexpr int kSmem = 1024 + kStages * kStage + kDrain * 1024 + 4 * 3072;   // and the draining and the scale warps' buffers
+    static constexpr int kSmem = 1024 + kStages * kStage + kDrain * 1024 + 12 * 1024;   // and the draining and the scale warps' buffers
 };
 constexpr uint32_t kScaleCol = 256;                                  // the first of them
 
@@ -524,10 +539,11 @@ extern "C" int mxfp4_matmul(const uint8_t* a, const uint8_t* a_scales, const uin
     if (!a || !a_scales || !b || !b_scales || !out) return MOE_ERR_INVALID_ARG;
     if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_scales, 4) || !aligned(b_scales, 4) || !aligned(out, 16))
         return MOE_ERR_MISALIGNED;
-    if (M > 16) {
-        int dev = 0, sms = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            return MOE_ERR_CUDA;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    const int64_t few = (N + 15) / 16;   // CTAs
+    if (M > 16 || few > (M <= 8 ? 2 : 1) * sms) {
         const int m = (int)M, n = (int)N, k = (int)K;
         // 64 columns a CTA while that is one wave (256 x 4096 x 4096: 9.8 us against 10.8 for 128).  Else 128, or 256 x 256
         // for a pair of CTAs: a wave of the latter takes 1.5 times as long (11.3 us against 7.5 at K = 4096) for up to twice
@@ -542,7 +558,7 @@ extern "C" int mxfp4_matmul(const uint8_t* a, const uint8_t* a_scales, const uin
         return narrow ? MOE_MM(64, MOE_BF16) : MOE_MM(128, MOE_BF16);
 #undef MOE_MM
     }
-    const unsigned grid = static_cast<unsigned>((N + 15) / 16);
+    const unsigned grid = static_cast<unsigned>(few);
 #define MOE_MF(NT, TYPE) mxmm::k_few<NT, TYPE><<<grid, 256, 0, stream>>>(a, a_scales, b, b_scales, (int)M, N, (int)K, out)
     if (out_type == MOE_F32) { if (M <= 8) MOE_MF(1, MOE_F32); else MOE_MF(2, MOE_F32); }
     else { if (M <= 8) MOE_MF(1, MOE_BF16); else MOE_MF(2, MOE_BF16); }

@@ -101,7 +101,8 @@ def _operands(g, M, N, K, spread=4):
 
 SHAPES = [(1, 1, 32), (1, 128, 32), (1, 4096, 4096), (2, 77, 96), (5, 1001, 2080), (8, 256, 1024), (9, 129, 4128),
           (16, 4096, 512), (17, 130, 160), (31, 64, 8192), (77, 1001, 2080), (127, 255, 224), (128, 128, 256),
-          (129, 257, 288), (200, 3, 64), (300, 1, 4096), (512, 640, 4096), (1025, 513, 1056), (2433, 2299, 544), (4097, 2600, 288)]
+          (129, 257, 288), (200, 3, 64), (300, 1, 4096), (512, 640, 4096), (1025, 513, 1056), (2433, 2299, 544), (4097, 2600, 288),
+          (8, 4736, 64), (1, 4800, 352), (12, 2401, 96)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])

@@ -510,25 +510,16 @@ __device__ __forceinline__ void DecodeWarp<kMx, kScaleSmem>::routed() {
             const int x = of[8 * n + i < n_tok ? 8 * n + i : 8 * n];
             return kDown ? x : (int)S.need_at[x];
         };
-        const int who0 = column(0, g), c00 = kMx ? 0 : column(0, col), c01 = kMx ? 0 : column(0, col + 1);
+        // a block's columns: its fragments' offset and its group sums'
+        const int who0 = column(0, g), o00 = kMx ? 0 : column(0, col) * pieces, o01 = kMx ? 0 : column(0, col + 1) * pieces;
+        const uint32_t at0 = frags + who0 * frag_row + t * 16;
         float acc[2][4] = {};
         for (int c = 0; c < R.chunks; ++c) {
             wait_full();
             const int first = c * R.cp, last = min(first + R.cp, R.pieces);
-#pragma unroll 1
-            for (int n = 0; ok && 8 * n < n_tok; ++n) {      // blocks of eight columns: nearly always one
-                const int who = n ? column(1, g) : who0;
-                const uint32_t at = frags + who * frag_row + t * 16;
+            auto block = [&](int who, uint32_t at, uint32_t o0, uint32_t o1, float (&a)[4]) {
                 const uint8_t* src = kGlobal ? p.hq + who * (int64_t)frag_row + t * 16 : nullptr;
-                uint32_t o0 = 0, o1 = 0;                     // group sums of the lane's two columns
-                if constexpr (!kMx) {
-                    o0 = (n ? column(1, col) : c00) * pieces;
-                    o1 = (n ? column(1, col + 1) : c01) * pieces;
-                }
                 uint32_t row = slots0 + slot * p.slot_bytes + r * 128;
-                float a[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = n ? acc[1][i] : acc[0][i];
 #pragma unroll 1
                 for (int piece = first; piece < last; ++piece, row += step) {
                     uint4 f[8];
@@ -562,10 +553,12 @@ __device__ __forceinline__ void DecodeWarp<kMx, kScaleSmem>::routed() {
                     const DecodeScales<kScaleSmem> s{sc.a + piece * (kMx ? 8 : 4), sc.b + piece * (kMx ? 8 : 4)};
                     piece_mma<kMx>(row, row + row_b, s, K / 128 - 2 * piece, f, off0, off1, a);
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    acc[0][i] = n ? acc[0][i] : a[i];
-                    acc[1][i] = n ? a[i] : acc[1][i];
+            };
+            if (ok) {
+                block(who0, at0, o00, o01, acc[0]);
+                if (n_tok > 8) {                             // (seldom: more than eight tokens)
+                    const int who = column(1, g);
+                    block(who, frags + who * frag_row + t * 16, kMx ? 0 : column(1, col) * pieces, kMx ? 0 : column(1, col + 1) * pieces, acc[1]);
                 }
             }
             release();

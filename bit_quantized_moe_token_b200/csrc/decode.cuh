@@ -12,24 +12,28 @@
 //
 //   prologue  (router form: the logits, a barrier.)  Every CTA ranks the logits itself, a warp a token, lists the touched
 //             experts and starts streaming; meanwhile the multiplying warps quantize the tokens that its experts need into
-//             B fragments in shared memory: f16 for up to six tokens, FP8 (widened at each use) beyond: at T = 16 three
-//             experts' tokens seldom are more, and the widening would cost every piece
+//             B fragments in shared memory: f16 for up to six tokens, FP8 (widened at each use) beyond, since a CTA's
+//             share of the experts (one to four of them) seldom has more
 //   gate/up   unit = 8 gate rows and the same 8 up rows of one touched expert, all of K; a phase's units are split evenly
 //             over the CTAs; h (fp32) goes to the workspace.  Then the shared experts' (bf16)
 //   barrier   each CTA quantizes the rows of h that its down units read into its own shared memory; where some CTA's rows
-//             do not fit, CTA r quantizes row r into the workspace and a second barrier follows (own rows: 41 us at T = 1
-//             against 44, the barrier)
+//             do not fit, CTA r quantizes row r into the workspace and a second barrier follows
 //   down      unit = 16 rows of one touched expert (then of a shared expert); gated rows to the workspace
 //   barrier   the rows are added in selection order
 //
 // Eight warps multiply and four stream for them.  A warp has rings of its own (two to four slots of 8 KB, chunks of 4
 // pieces of 16 rows x 128 bytes in the 128-byte swizzle, one TMA box a row set), so that no warp waits for another's data;
 // a streaming warp has a lane for each ring it feeds.  Issued by the multiplying warps themselves a chunk's copies cost
-// them some 1,000 cycles.  Other divisions, in us for W4A8 (T = 1, 8, 16) and MXFP4 (T = 1, 8):
-//   8 + 4 warps   38.6  138  288   41  138        12 + 4   36.9  146  336   40  146
-//   9 + 3         40.3  143  333   44  154        10 + 2   39.6  145  339   44  163
-// and the loop over a chunk's pieces unrolled twice (rolled it stays in the instruction cache): 40.1 144 300 43 142.
-// A row's scales come beside its unit's first chunk where the buffers fit, else they are read in place.
+// them some 1,000 cycles.  A row's scales come beside its unit's first chunk where the buffers fit, else they are read in
+// place.  Measured, in us for W4A8 (T = 1, 8 and 16) and MXFP4 (T = 1 and 8) at the sizes below:
+//   8 + 4 warps                          37.8  137  285   41  138
+//   12 + 4 (chunks of two pieces)        36.9  146  336   40  146
+//   9 + 3                                40.3  143  333   44  154
+//   10 + 2                               39.6  145  339   44  163
+//   rows of h always by the workspace    40.9  148  314   44  150
+//   scales always in place               41.7  151  313   46  158
+//   fragments always FP8                 39.3  146  304   43  148
+//   pieces unrolled twice                40.1  144  300   43  142   (rolled, the loop stays in the instruction cache)
 //
 // The products run on mma.sync m16n8k16 (f16, fp32 sums): a unit's 16 rows are the M, up to eight tokens the N.  tcgen05
 // would put 128 rows a tile, and the widened weights through TMEM, for the same eight columns.  E4M3 values are exact in
@@ -42,12 +46,14 @@
 // sum is scaled in fp32 by its weight scale: one promotion every 128 (32) weights.  Shared experts run on the bf16 MMA,
 // their activation as bf16 hi + lo halves (16 bits of it).
 //
-// Measured, E = 256, top 6, H = 4096, N = 2048: W4A8 T = 1 38.6 us (78 MB: 31 % of HBM's measured 6.56 TB/s), T = 8 with
-// the router 138 us (578 MB: 64 %), T = 16 with two shared experts 288 us (1.15 GB: 61 %); MXFP4 T = 1 with the router
-// 41 us, T = 8 138 us (593 MB: 65 %).  At T = 1 the chain is: lists 4.6 us, tokens quantized 9.5, gate/up 22.5, barrier
-// 24.8, h quantized 26.5, down 32.6, sums 35.  At T = 8 the same grid reads the bytes in 104 us when nothing is
-// multiplied; a warp needs some 640 cycles a piece (widening, fragments, MMAs, promotion), eight of them 80 cycles for
-// 2 KB, which is just the rate at which HBM delivers them.
+// Measured, E = 256, top 6, H = 4096, N = 2048: W4A8 T = 1 37.8 us (78 MB: 31 % of HBM's measured 6.56 TB/s), T = 8 with
+// the router 137 us (578 MB: 64 %), T = 16 with two shared experts 285 us (1.15 GB: 61 %); MXFP4 T = 1 with the router
+// 41 us (31 %), T = 8 138 us (593 MB: 66 %).  At T = 1 the chain is: lists 4.6 us, tokens quantized 9.5, gate/up 22,
+// barrier 24, h quantized 26, down 32, sums 34.  At T = 8 the same grid reads the bytes in 104 us when nothing is
+// multiplied, and the multiplying warps find their chunks there (they wait 5 % of the gate/up phase): what they are short
+// of is issue slots.  A piece is some 200 warp instructions (80 of them the widening's half-rate logic) in 640 cycles, two
+// warps a scheduler.  Loading half a piece ahead of the MMAs (147 us), or addresses that run from piece to piece (145),
+// hide latency but add instructions.
 #pragma once
 #include <cooperative_groups.h>
 #include <type_traits>

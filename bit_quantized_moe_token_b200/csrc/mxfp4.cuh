@@ -12,7 +12,11 @@
 // not depend on rounding.  Both directions are bound by HBM: 2 (4) bytes read and 17/32 written a
 // value, and the reverse.  Four threads share a block: each takes eight values with one or two
 // 16-byte loads (consecutive threads read consecutive chunks) and the block's maximum goes
-// through two shuffles.
+// through two shuffles.  A thread has four such chunks in flight.
+//
+// Measured: 16384 x 4096 bf16 quantized and read back in 57 us (340 MB: 91 % of HBM's measured 6.56
+// TB/s; with one chunk a thread 80 us); 1000 x 4128 fp32 rows of a wider buffer in 6.9 us, 8 x 4096
+// in 3.4: two launches, which is what a few rows cost.
 #pragma once
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>

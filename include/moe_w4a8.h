@@ -549,8 +549,8 @@ typedef struct {
  *   x_bf16 [T, H]   router_logits [T, E] fp32 or wr_bf16 [E, H]   out_bf16 [T, H] (may be x_bf16)
  *   ws, ws_bytes    device scratch, >= the _workspace_bytes of the layer, T and k; 256-byte
  *                   aligned, contents on entry ignored; calls that may overlap need their own
- * Shapes as moe_w4a8_forward with T <= 16, shared_N <= 8192 and H * ceil(T / 8) <= 16384.  Weight
- * and scale pointers are 16-byte aligned.  T == 0 is a no-op.  The _workspace_bytes calls return 0
+ * Shapes as moe_w4a8_forward with T <= 16, shared_N <= 8192, n_shared <= 64 and
+ * H * ceil(T / 8) <= 16384.  Weight and scale pointers are 16-byte aligned.  T == 0 is a no-op.  The _workspace_bytes calls return 0
  * for what the layer call refuses.
  * --------------------------------------------------------------------------------------- */
 size_t moe_w4a8_decode_workspace_bytes(const moe_w4a8_layer* layer, int64_t T, int k);

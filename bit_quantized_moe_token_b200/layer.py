@@ -131,40 +131,58 @@ def forward(layer, x, logits, k: int, out=None, ws=None, stream=None):
     return out
 
 
+def _on(stream):
+    """The context of a stream (torch stream or handle): what a wrapper allocates or copies then belongs to the stream
+    that its kernels run on, and scratch freed on return is not handed out while they still use it."""
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 def quant_mxfp4(x, stream=None):
     """bf16, f16 or fp32 values [..., K] on the GPU -> (E2M1 codes uint8 [..., K/2], E8M0 scales
     uint8 [..., K/32]).  Two-dimensional x may have strided rows."""
+    if stream is not None:
+        with _on(stream):
+            return quant_mxfp4(x)
     import torch
     if x.dim() != 2:
-        codes, scales = quant_mxfp4(x.reshape(-1, x.shape[-1]), stream=stream)
+        codes, scales = quant_mxfp4(x.reshape(-1, x.shape[-1]))
         return codes.view(*x.shape[:-1], -1), scales.view(*x.shape[:-1], -1)
     rows, K = x.shape
     if K % 32:
         raise ValueError("K must be a multiple of 32")
     codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
     scales = torch.empty((rows, K // 32), dtype=torch.uint8, device=x.device)
-    mxfp4_quant_rows(x, codes, scales, stream=stream)
+    mxfp4_quant_rows(x, codes, scales)
     return codes, scales
 
 
 def dequant_mxfp4(codes, scales, dtype=None, stream=None):
     """The values [..., K] of MXFP4 codes [..., K/2] and scales [..., K/32], bf16 (the default) or
     fp32, both exact."""
+    if stream is not None:
+        with _on(stream):
+            return dequant_mxfp4(codes, scales, dtype)
     import torch
     if codes.dim() != 2:
-        y = dequant_mxfp4(codes.reshape(-1, codes.shape[-1]), scales.reshape(-1, scales.shape[-1]), dtype, stream=stream)
+        y = dequant_mxfp4(codes.reshape(-1, codes.shape[-1]), scales.reshape(-1, scales.shape[-1]), dtype)
         return y.view(*codes.shape[:-1], -1)
     y = torch.empty((codes.shape[0], 2 * codes.shape[1]), dtype=dtype or torch.bfloat16, device=codes.device)
-    mxfp4_dequant_rows(codes, scales, y, stream=stream)
+    mxfp4_dequant_rows(codes, scales, y)
     return y
 
 
 def matmul_mxfp4(a, a_scales, b, b_scales, dtype=None, out=None, stream=None):
     """A B^T [M, N] of MXFP4 rows A [M, K] and B [N, K], as bf16 (the default) or fp32."""
+    if stream is not None:
+        with _on(stream):
+            return matmul_mxfp4(a, a_scales, b, b_scales, dtype, out)
     import torch
     if out is None:
         out = torch.empty(a.shape[0], b.shape[0], dtype=dtype or torch.bfloat16, device=a.device)
-    mxfp4_matmul(a, a_scales, b, b_scales, out, stream=stream)
+    mxfp4_matmul(a, a_scales, b, b_scales, out)
     return out
 
 
@@ -190,22 +208,28 @@ def alloc_decode_workspace(layer, T: int, k: int, device=None):
 
 def decode(layer, x, logits, k: int, out=None, ws=None, stream=None):
     """The whole layer on up to 16 tokens (Layer: W4A8, LayerMX: MXFP4) from router logits [T, E]."""
+    if stream is not None:
+        with _on(stream):
+            return decode(layer, x, logits, k, out, ws)
     import torch
     if out is None:
         out = torch.empty_like(x)
     if ws is None:
         ws = alloc_decode_workspace(layer, x.shape[0], k, x.device)
-    (moe_mxfp4_decode if isinstance(layer, LayerMX) else moe_w4a8_decode)(layer, x, logits, k, out, ws, stream=stream)
+    (moe_mxfp4_decode if isinstance(layer, LayerMX) else moe_w4a8_decode)(layer, x, logits, k, out, ws)
     return out
 
 
 def decode_router(layer, x, wr, k: int, out=None, ws=None, stream=None):
     """decode() with the logits computed from the router weight wr [E, H]."""
+    if stream is not None:
+        with _on(stream):
+            return decode_router(layer, x, wr, k, out, ws)
     import torch
     if out is None:
         out = torch.empty_like(x)
     if ws is None:
         ws = alloc_decode_workspace(layer, x.shape[0], k, x.device)
     fn = moe_mxfp4_decode_router if isinstance(layer, LayerMX) else moe_w4a8_decode_router
-    fn(layer, x, wr, k, out, ws, stream=stream)
+    fn(layer, x, wr, k, out, ws)
     return out

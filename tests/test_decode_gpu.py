@@ -216,6 +216,40 @@ def test_two_streams_at_once(moe, fmt):
     assert moe.moe_last_device_status() == 0
 
 
+@pytest.mark.parametrize("fmt", FMT)
+def test_scratch_of_a_call_on_another_stream(moe, fmt):
+    """Without a workspace of its own the call takes one that the current stream's next allocations do not get."""
+    c = Case(moe, fmt, 64, 2048, 1024, 18)
+    x, lg = c.tokens(4)
+    wr = (torch.randn(64, 2048, generator=c.g, device="cuda") / 45.0).bfloat16()
+    want, routed = moe.decode(c.layer, x, lg, 6), moe.decode_router(c.layer, x, wr, 6)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for at in (s, s.cuda_stream):
+        outs = []
+        for _ in range(10):
+            outs.append((moe.decode(c.layer, x, lg, 6, stream=at), moe.decode_router(c.layer, x, wr, 6, stream=at)))
+            n = moe.alloc_decode_workspace(c.layer, 4, 6).fill_(0xFF).numel()
+        torch.cuda.synchronize()
+        assert n > 0
+        for a, b in outs:
+            assert torch.equal(a, want) and torch.equal(b, routed)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_token_that_is_not_finite_stays_alone(moe, fmt, bad):
+    """Its own outputs are NaN; its neighbours' on the same experts are, bit for bit, what they were."""
+    c = Case(moe, fmt, 6, 512, 256, 19, n_shared=1)
+    x, lg = c.tokens(9)
+    want = moe.decode(c.layer, x, lg, 3)
+    x[4, 17] = bad
+    got = moe.decode(c.layer, x, lg, 3)
+    rest = [t for t in range(9) if t != 4]
+    assert torch.equal(got[rest], want[rest])
+    assert torch.isnan(got[4]).all()
+
+
 def test_agrees_with_the_forward(moe):
     """On W4A8 weights the few-token layer and moe_w4a8_forward compute the same layer: both within the tolerance."""
     c = Case(moe, "w4a8", 64, 2048, 1024, 16, n_shared=2, Ns=512)

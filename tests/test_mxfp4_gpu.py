@@ -151,7 +151,7 @@ def test_matmul_leaves_what_lies_beside_its_output(moe, M, N):
     assert ((out.double() - ref).abs() <= plain64.matmul_tolerance(va, vb, ref, torch.float32)).all()
 
 
-@pytest.mark.parametrize("M", [1, 12, 260])
+@pytest.mark.parametrize("M", [1, 12, 260, 8000])
 def test_matmul_repeats_bit_for_bit_captured_and_on_another_stream(moe, M):
     a, sa, b, sb = _operands(_gen(4), M, 520, 2048)
     first = moe.matmul_mxfp4(a, sa, b, sb)
@@ -168,6 +168,30 @@ def test_matmul_repeats_bit_for_bit_captured_and_on_another_stream(moe, M):
         out.zero_()
         graph.replay()
         assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_on_another_stream_everything_runs_there(moe, handle):
+    """What the wrappers copy and allocate for a call on a stream does not wait for, or race with, the current one."""
+    g = _gen(6)
+    x = torch.randn(64, 8, 256, generator=g, device="cuda").bfloat16()
+    w = torch.randn(96, 256, generator=g, device="cuda").bfloat16()
+    qw, turned = moe.quant_mxfp4(w), x.transpose(0, 1)
+    want = moe.quant_mxfp4(turned.contiguous())
+    product = moe.matmul_mxfp4(want[0][0], want[1][0], *qw)
+    values = moe.dequant_mxfp4(*want)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    at = s.cuda_stream if handle else s
+    torch.cuda._sleep(100_000_000)                       # the current stream is busy for some 50 ms
+    c, e = moe.quant_mxfp4(turned, stream=at)
+    y = moe.dequant_mxfp4(c, e, stream=at)
+    p = moe.matmul_mxfp4(c[0], e[0], *qw, stream=at)
+    s.synchronize()
+    assert not torch.cuda.current_stream().query()
+    c, e, y, p = (t.cpu() for t in (c, e, y, p))
+    assert torch.equal(c, want[0].cpu()) and torch.equal(e, want[1].cpu())
+    assert torch.equal(y, values.cpu()) and torch.equal(p, product.cpu())
 
 
 def test_empty(moe):

@@ -281,12 +281,13 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map,
 
 template <int BN, int kType, bool kPair>
 __global__ void __launch_bounds__(Cfg<BN, kPair>::kThreads, 1) k_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                                                      const __grid_constant__ CUtensorMap map_as, const __grid_constant__ CUtensorMap map_bs, bool boxes,
                                                       const uint8_t* __restrict__ as, const uint8_t* __restrict__ bs, int M, int N, int K,
                                                       void* __restrict__ out) {
     using C = Cfg<BN, kPair>;
     constexpr int kRows = kPair ? 256 : 128;   // of A in a tile
     extern __shared__ __align__(16) uint8_t raw[];
-    __shared__ uint64_t full[C::kStages], empty[C::kStages], acc_full, acc_empty;
+    __shared__ uint64_t full[C::kStages], empty[C::kStages], sc_full[2], sc_empty[2], acc_full, acc_empty;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort;
     const uint32_t base = (tc::smem_u32(raw) + 1023u) & ~1023u;
@@ -303,6 +304,10 @@ __global__ void __launch_bounds__(Cfg<BN, kPair>::kThreads, 1) k_gemm(const __gr
             tc::mbar_init(&full[i], 1 + (kPair ? 8 : 4));   // the bytes, and the scale warps
             tc::mbar_init(&empty[i], 1);
         }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&sc_full[i], 1);
+            tc::mbar_init(&sc_empty[i], 4);
+        }
         tc::mbar_init(&acc_full, 1);
         tc::mbar_init(&acc_empty, (kPair ? 2 : 1) * C::kDrain);
         tc::fence_mbar_init();
@@ -312,6 +317,10 @@ __global__ void __launch_bounds__(Cfg<BN, kPair>::kThreads, 1) k_gemm(const __gr
     if (warp == C::kDrain + 4 && lane == 0) {
         ws::prefetch_map(&map_a);
         ws::prefetch_map(&map_b);
+        if (boxes) {
+            ws::prefetch_map(&map_as);
+            ws::prefetch_map(&map_bs);
+        }
     }
     tc::tc_fence_before();
     if constexpr (kPair) cluster_sync();
@@ -322,10 +331,20 @@ __global__ void __launch_bounds__(Cfg<BN, kPair>::kThreads, 1) k_gemm(const __gr
 
     if (warp == C::kDrain + 4) {
         if (elected()) {
+            uint32_t pair = 0;
             ws::Ring<C::kStages> r;
             for (int tile = tile0; ok && tile < tiles; tile += tile_step) {
                 const int m0 = tile / tn * kRows + rank * 128, n0 = tile % tn * BN + rank * C::kBRows;
                 for (int s = 0; s < stages; ++s, r.next()) {
+                    if (boxes && (s & 1) == 0) {   // the scales of this stage and the next
+                        if (!(ok = ws::wait(&sc_empty[pair & 1u], ((pair >> 1) & 1u) ^ 1u, &abort))) break;
+                        uint64_t* bar = &sc_full[pair & 1u];
+                        uint8_t* to = raw + (base - tc::smem_u32(raw)) + C::kStages * C::kStage + C::kDrain * 1024 + (pair & 1u) * 6144;
+                        tc::mbar_arrive_expect_tx(bar, 2048 * (1 + C::kHalves));
+                        ws::tma_load_2d(to, &map_as, s * 8, m0, bar);
+                        ws::tma_load_2d(to + 2048, &map_bs, s * 8, tile % tn * BN, bar);
+                        ++pair;
+                    }
                     if (!(ok = ws::wait(&empty[r.idx], r.phase ^ 1u, &abort))) break;
                     if (rank == 0) tc::mbar_arrive_expect_tx(&full[r.idx], (kPair ? 2 : 1) * C::kStage);
                     uint8_t* dst = raw + (base - tc::smem_u32(raw)) + r.idx * C::kStage;
@@ -367,7 +386,46 @@ __global__ void __launch_bounds__(Cfg<BN, kPair>::kThreads, 1) k_gemm(const __gr
         const int w = warp - C::kDrain;
         uint8_t* buf = raw + (base - tc::smem_u32(raw)) + C::kStages * C::kStage + C::kDrain * 1024;   // two pairs of stages
         ws::Ring<C::kStages> r;
-        bool well = true;   // of all four warps
+        auto put = [&](uint32_t column, const uint4& v) {   // four columns of the stage's
+            tmem_st4(tmem + (static_cast<uint32_t>(w * 32) << 16) + kScaleCol + r.idx * C::kCols + column, v);
+        };
+        auto stored = [&] {
+            tc::tmem_wait_st();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (kPair) arrive_first(&full[r.idx]);
+                else tc::mbar_arrive(&full[r.idx]);
+            }
+            r.next();
+        };
+        if (boxes) {
+            uint32_t pair = 0;
+            for (int tile = tile0; ok && tile < tiles; tile += tile_step)
+                for (int s = 0; ok && s < stages; s += 2, ++pair) {
+                    if (!(ok = __all_sync(~0u, ws::wait(&sc_full[pair & 1u], (pair >> 1) & 1u, &abort)))) break;
+                    const uint8_t* from = buf + (pair & 1u) * 6144 + lane * 16;
+                    uint4 v[4 * (1 + C::kHalves)];           // rows lane, 32 + lane ..: the two stages' words
+#pragma unroll
+                    for (int i = 0; i < 4 * (1 + C::kHalves); ++i) v[i] = *reinterpret_cast<const uint4*>(from + 512 * i);
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&sc_empty[pair & 1u]);
+#pragma unroll
+                    for (int d = 0; d < 2; ++d) {
+                        if (!(ok = __all_sync(~0u, ws::wait(&empty[r.idx], r.phase ^ 1u, &abort)))) break;
+                        tc::tc_fence_after();
+#pragma unroll
+                        for (int i = 0; i < 1 + C::kHalves; ++i) {
+                            const uint4 *q = v + 4 * i;
+                            put(i ? 8 + 4 * (i - 1) : 0, d ? make_uint4(q[0].z, q[1].z, q[2].z, q[3].z) : make_uint4(q[0].x, q[1].x, q[2].x, q[3].x));
+                            put(i ? 8 + 4 * (C::kHalves + i - 1) : 4,
+                                d ? make_uint4(q[0].w, q[1].w, q[2].w, q[3].w) : make_uint4(q[0].y, q[1].y, q[2].y, q[3].y));
+                        }
+                        stored();
+                    }
+                }
+        }
+        bool well = !boxes;   // (all four warps')
         uint32_t turn = 0;
         for (int tile = tile0; well && tile < tiles; tile += tile_step) {
             const int m = tile / tn * kRows + rank * 128 + 32 * w + lane, n = tile % tn * BN + 32 * w + lane;
@@ -399,23 +457,16 @@ __global__ void __launch_bounds__(Cfg<BN, kPair>::kThreads, 1) k_gemm(const __gr
                     }
                     if (!(well = all_well(ok))) break;
                     load(s0 / 2 + d + kAhead, v[d]);
-                    for (int s = s0 + 2 * d; ok && s < min(s0 + 2 * d + 2, stages); ++s, r.next()) {
+                    for (int s = s0 + 2 * d; ok && s < min(s0 + 2 * d + 2, stages); ++s) {
                         if (!(ok = __all_sync(~0u, ws::wait(&empty[r.idx], r.phase ^ 1u, &abort)))) break;
                         tc::tc_fence_after();
-                        const uint32_t to = tmem + (static_cast<uint32_t>(w * 32) << 16) + kScaleCol + r.idx * C::kCols;
                         const uint8_t* from = of + (s & 1) * 1024;
 #pragma unroll
                         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
                             for (int i = 0; i < 1 + C::kHalves; ++i)
-                                tmem_st4(to + (i ? 8 + 4 * (kb * C::kHalves + i - 1) : 4 * kb), *reinterpret_cast<const uint4*>(from + 2048 * i + 512 * kb));
-                        tc::tmem_wait_st();
-                        tc::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if constexpr (kPair) arrive_first(&full[r.idx]);
-                            else tc::mbar_arrive(&full[r.idx]);
-                        }
+                                put(i ? 8 + 4 * (kb * C::kHalves + i - 1) : 4 * kb, *reinterpret_cast<const uint4*>(from + 2048 * i + 512 * kb));
+                        stored();
                     }
                 }
             }
@@ -501,9 +552,12 @@ template <int BN, int kType, bool kPair = false>
 inline int launch(const uint8_t* a, const uint8_t* as, const uint8_t* b, const uint8_t* bs, int M, int N, int K, void* out, int sms,
                   cudaStream_t stream) {
     using C = Cfg<BN, kPair>;
-    CUtensorMap ma, mb;
+    CUtensorMap ma, mb, mas = {}, mbs = {};
+    const bool boxes = K % 512 == 0 && aligned(as, 16) && aligned(bs, 16);
     if (!make_map_u8(&ma, a, K / 2, M, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map_u8(&mb, b, K / 2, N, 128, C::kBRows, CU_TENSOR_MAP_SWIZZLE_128B))
+        !make_map_u8(&mb, b, K / 2, N, 128, C::kBRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        (boxes && (!make_map_u8(&mas, as, K / kMxBlock, M, 16, 128, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+                   !make_map_u8(&mbs, bs, K / kMxBlock, N, 16, 128 * C::kHalves, CU_TENSOR_MAP_SWIZZLE_NONE))))
         return MOE_ERR_CUDA;
     const void* fn = reinterpret_cast<const void*>(k_gemm<BN, kType, kPair>);
     if (set_smem(fn, C::kSmem)) return MOE_ERR_CUDA;
@@ -520,7 +574,7 @@ inline int launch(const uint8_t* a, const uint8_t* as, const uint8_t* b, const u
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, k_gemm<BN, kType, kPair>, ma, mb, as, bs, M, N, K, out) == cudaSuccess) return MOE_OK;
+    if (cudaLaunchKernelEx(&cfg, k_gemm<BN, kType, kPair>, ma, mb, mas, mbs, boxes, as, bs, M, N, K, out) == cudaSuccess) return MOE_OK;
     (void)cudaGetLastError();   // a rejected launch leaves no error behind for later calls
     return MOE_ERR_CUDA;
 }

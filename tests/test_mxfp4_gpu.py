@@ -102,7 +102,7 @@ def _operands(g, M, N, K, spread=4):
 SHAPES = [(1, 1, 32), (1, 128, 32), (1, 4096, 4096), (2, 77, 96), (5, 1001, 2080), (8, 256, 1024), (9, 129, 4128),
           (16, 4096, 512), (17, 130, 160), (31, 64, 8192), (77, 1001, 2080), (127, 255, 224), (128, 128, 256),
           (129, 257, 288), (200, 3, 64), (300, 1, 4096), (512, 640, 4096), (1025, 513, 1056), (2433, 2299, 544), (4097, 2600, 288),
-          (8, 4736, 64), (1, 4800, 352), (12, 2401, 96)]
+          (8, 4736, 64), (1, 4800, 352), (12, 2401, 96), (2500, 2300, 1024), (130, 70, 512)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -114,6 +114,20 @@ def test_matmul(moe, M, N, K, dtype):
     ref = va @ vb.T
     assert got.dtype == dtype
     assert ((got.double() - ref).abs() <= plain64.matmul_tolerance(va, vb, ref, dtype)).all()
+
+
+@pytest.mark.parametrize("M,N", [(3, 40), (50, 90), (2500, 2300)])
+def test_matmul_scales_at_any_whole_word(moe, M, N):
+    """Scales 4 bytes past a 16-byte boundary, which the wide loads do not take: the same product."""
+    a, sa, b, sb = _operands(_gen(8), M, N, 512)
+    want = moe.matmul_mxfp4(a, sa, b, sb)
+    off = []
+    for s in (sa, sb):
+        buf = torch.full((s.numel() + 16,), 0xFF, dtype=torch.uint8, device="cuda")
+        buf[4:4 + s.numel()] = s.flatten()
+        off.append(buf[4:4 + s.numel()].view(s.shape))
+    assert torch.equal(moe.matmul_mxfp4(a, off[0], b, sb), want)
+    assert torch.equal(moe.matmul_mxfp4(a, sa, b, off[1]), want)
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 300, 256), (150, 300, 320)])

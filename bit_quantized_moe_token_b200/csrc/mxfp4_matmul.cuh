@@ -144,10 +144,13 @@ __global__ void __launch_bounds__(256) k_few(const uint8_t* __restrict__ a, cons
 // Roles: kDrain warps drain the accumulator, four bring the scales, one thread issues the TMA loads, one the MMAs.
 //
 // Scales.  The tensor core wants 128 rows' four scales of 128 codes as four TMEM columns: row 32 c + l in lane l of
-// column c, the same in all four lane quadrants.  No TMA box is as narrow as a row's eight bytes a stage, so the scale
-// warps read 16 bytes a row (two stages) two such pairs ahead, exchange them through shared memory and each stores its
-// quadrant's columns with tcgen05.st.  (tcgen05.cp from shared memory, issued ahead of the stage's MMAs, held up the MMAs:
-// 16384 x 4096 x 4096 in 173 us against 156.)
+// column c, the same in all four lane quadrants; each scale warp stores its quadrant's with tcgen05.st.  (tcgen05.cp from
+// shared memory, issued ahead of the stage's MMAs, held those up: 16384 x 4096 x 4096 in 173 us against 156.)  They come
+// as TMA boxes of 16 bytes (two stages) of every row; where K, the pointers or M do not suit those, the warps load the
+// same 16 bytes a row two such pairs ahead and exchange them through shared memory.  With these loads everywhere the
+// product takes 135 us against 115: a load of 32 rows is 32 passes of the shared memory's data path, which is what the
+// kernel is short of (a stage's codes are written once and read once, 512 cycles of it; by loads and exchange the
+// scales took 335 more, now 120).
 //
 // The issuing thread.  What it does a stage has to take less than the stage's 512 cycles of MMA: one barrier for the bytes
 // and the scales, and a thread chosen by elect.sync, whose operands the compiler keeps in uniform registers (with two
@@ -157,9 +160,8 @@ __global__ void __launch_bounds__(256) k_few(const uint8_t* __restrict__ a, cons
 // into registers (rounded to the output type), free it, and store while the next tile's MMAs run: sixteen warps of 64
 // columns, whose registers suffice without spills (eight of 128: 144 us against 136).
 //
-// Measured (bf16 out): 16384 x 4096 x 4096 135 us = 4,070 TFLOP/s, 2.4 times the measured bf16 peak (FP4's nominal rate is
-// four times bf16's); K = 8192 4,490; 2048 x 4096 x 4096 24.3 us: two waves for 1.73 waves of tiles.  Without the drain's
-// stores the first takes 123 us, without MMAs for half of K 110: the rest is the fill and drain of each tile.
+// Measured (bf16 out): 16384 x 4096 x 4096 115 us = 4,770 TFLOP/s, 2.85 times the measured bf16 peak (FP4's nominal rate
+// is four times bf16's); K = 8192 5,170 TFLOP/s; 2048 x 4096 x 4096 19.2 us: two waves for 1.73 waves of tiles.
 namespace mxmm {
 
 constexpr int kStageK = 256;
@@ -553,7 +555,9 @@ inline int launch(const uint8_t* a, const uint8_t* as, const uint8_t* b, const u
                   cudaStream_t stream) {
     using C = Cfg<BN, kPair>;
     CUtensorMap ma, mb, mas = {}, mbs = {};
-    const bool boxes = K % 512 == 0 && aligned(as, 16) && aligned(bs, 16);
+    // scales by TMA: rows of whole 16-byte pieces.  (Few tokens: rows outside the tensor cost the boxes more than loads
+    // that skip them; 16 x 14336 x 4096 took 16.4 us against 14.6, 64 x 4096 x 4096 8.5 against 9.3.)
+    const bool boxes = K % 512 == 0 && aligned(as, 16) && aligned(bs, 16) && M >= 64;
     if (!make_map_u8(&ma, a, K / 2, M, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map_u8(&mb, b, K / 2, N, 128, C::kBRows, CU_TENSOR_MAP_SWIZZLE_128B) ||
         (boxes && (!make_map_u8(&mas, as, K / kMxBlock, M, 16, 128, CU_TENSOR_MAP_SWIZZLE_NONE) ||
@@ -599,9 +603,9 @@ extern "C" int mxfp4_matmul(const uint8_t* a, const uint8_t* a_scales, const uin
     const int64_t few = (N + 15) / 16;   // CTAs
     if (M > 16 || few > (M <= 8 ? 2 : 1) * sms) {
         const int m = (int)M, n = (int)N, k = (int)K;
-        // 64 columns a CTA while that is one wave (256 x 4096 x 4096: 9.8 us against 10.8 for 128).  Else 128, or 256 x 256
-        // for a pair of CTAs: a wave of the latter takes 1.5 times as long (11.3 us against 7.5 at K = 4096) for up to twice
-        // the outputs (512 rows x 4096: 11.0 us against 14.9; 1024: 19.0 against 15.9; 2048: 32.9 against 26.2).
+        // 64 columns a CTA while that is one wave (256 x 4096 x 4096: 8.8 us against 9.7 for 128).  Else 128, or 256 x 256
+        // for a pair of CTAs: a wave of the latter takes 1.6 times as long (8.3 us against 5.2 at K = 4096) for up to twice
+        // the outputs (512 rows x 4096: 10.4 us against 12.9; 1024: 15.5 against 13.9; 2048: 25.8 against 21.2).
         const int64_t rows = (M + 127) / 128, t128 = rows * ((N + 127) / 128), t256 = (M + 255) / 256 * ((N + 255) / 256);
         const bool narrow = rows * ((N + 63) / 64) <= sms;
         if (!narrow && 3 * ((t256 + sms / 2 - 1) / (sms / 2)) <= 2 * ((t128 + sms - 1) / sms))

@@ -184,6 +184,22 @@ def test_matmul_repeats_bit_for_bit_captured_and_on_another_stream(moe, M):
         assert torch.equal(out, first)
 
 
+def test_matmul_two_streams_at_once(moe):
+    """Products that overlap, one of them with both operands the same rows."""
+    a, sa, b, sb = _operands(_gen(7), 2304, 2560, 1024)
+    sets = [((a, sa, b, sb), torch.cuda.Stream()), ((a, sa, a, sa), torch.cuda.Stream())]
+    want = [moe.matmul_mxfp4(*ops, dtype=torch.float32) for ops, _ in sets]
+    got = [torch.zeros_like(w) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (ops, s), out in zip(sets, got):
+            moe.matmul_mxfp4(*ops, out=out, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(got[1], got[1].T)
+    assert moe.moe_last_device_status() == 0
+
+
 @pytest.mark.parametrize("handle", [False, True])
 def test_on_another_stream_everything_runs_there(moe, handle):
     """What the wrappers copy and allocate for a call on a stream does not wait for, or race with, the current one."""

@@ -153,8 +153,8 @@ def quant_mxfp4(x, stream=None):
     rows, K = x.shape
     if K % 32:
         raise ValueError("K must be a multiple of 32")
-    codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((rows, K // 32), dtype=torch.uint8, device=x.device)
+    codes = x.new_empty((rows, K // 2), dtype=torch.uint8)
+    scales = x.new_empty((rows, K // 32), dtype=torch.uint8)
     mxfp4_quant_rows(x, codes, scales)
     return codes, scales
 
@@ -169,7 +169,7 @@ def dequant_mxfp4(codes, scales, dtype=None, stream=None):
     if codes.dim() != 2:
         y = dequant_mxfp4(codes.reshape(-1, codes.shape[-1]), scales.reshape(-1, scales.shape[-1]), dtype)
         return y.view(*codes.shape[:-1], -1)
-    y = torch.empty((codes.shape[0], 2 * codes.shape[1]), dtype=dtype or torch.bfloat16, device=codes.device)
+    y = codes.new_empty((codes.shape[0], 2 * codes.shape[1]), dtype=dtype or torch.bfloat16)
     mxfp4_dequant_rows(codes, scales, y)
     return y
 

@@ -26,7 +26,7 @@
 // a streaming warp has a lane for each ring it feeds.  Issued by the multiplying warps themselves a chunk's copies cost
 // them some 1,000 cycles.  A row's scales come beside its unit's first chunk where the buffers fit, else they are read in
 // place.  Measured, in us for W4A8 (T = 1, 8 and 16) and MXFP4 (T = 1 and 8) at the sizes below:
-//   8 + 4 warps                          37.8  137  285   41  138
+//   8 + 4 warps                          38.8  137  285   41  138
 //   12 + 4 (chunks of two pieces)        36.9  146  336   40  146
 //   9 + 3                                40.3  143  333   44  154
 //   10 + 2                               39.6  145  339   44  163
@@ -46,7 +46,7 @@
 // sum is scaled in fp32 by its weight scale: one promotion every 128 (32) weights.  Shared experts run on the bf16 MMA,
 // their activation as bf16 hi + lo halves (16 bits of it).
 //
-// Measured, E = 256, top 6, H = 4096, N = 2048: W4A8 T = 1 37.8 us (78 MB: 31 % of HBM's measured 6.56 TB/s), T = 8 with
+// Measured, E = 256, top 6, H = 4096, N = 2048: W4A8 T = 1 38.8 us (78 MB: 31 % of HBM's measured 6.56 TB/s), T = 8 with
 // the router 137 us (578 MB: 64 %), T = 16 with two shared experts 285 us (1.15 GB: 61 %); MXFP4 T = 1 with the router
 // 41 us (31 %), T = 8 138 us (593 MB: 66 %).  At T = 1 the chain is: lists 4.6 us, tokens quantized 9.5, gate/up 22,
 // barrier 24, h quantized 26, down 32, sums 34.  At T = 8 the same grid reads the bytes in 104 us when nothing is
@@ -474,7 +474,9 @@ struct DecodeWarp {
     uint32_t parity = 0;
     bool ok = true;
 
-    __device__ __forceinline__ void wait_full() { ok = ok && ws::wait(&S.full[warp][slot], parity, &S.abort); }
+    __device__ __forceinline__ void wait_full() {   // (the warp goes on or gives up as one)
+        if (ok) ok = __all_sync(0xffffffffu, ws::wait(&S.full[warp][slot], parity, &S.abort));
+    }
     __device__ __forceinline__ void release() {
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&S.empty[warp][slot]);

@@ -168,7 +168,8 @@ constexpr int kStageK = 256;
 
 template <int BN, bool kPair>
 struct Cfg {
-    static constexpr int kStages = kPair ? 6 : BN == 256 ? 4 : BN == 128 ? 6 : 8;
+    static_assert(kPair ? BN == 256 : BN <= 128);
+    static constexpr int kStages = BN >= 128 ? 6 : 8;
     static constexpr int kDrain = BN == 256 ? 16 : 8;                // warps that drain the accumulator
     static constexpr int kThreads = (kDrain + 6) * 32;
     static constexpr int kBRows = kPair ? BN / 2 : BN;               // of B in this CTA's shared memory

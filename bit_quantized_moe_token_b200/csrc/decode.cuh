@@ -327,6 +327,17 @@ __device__ __forceinline__ void rank_row(const float* l, int E, int k, int* ids,
     if (lane < k) gates[lane] = __fdiv_rn(mine, sum);
 }
 
+// Row maxima are taken over the bits of the magnitudes: as integers they order like the values, and a NaN is the largest,
+// so a row that holds one gets a scale and codes of NaN, and not the scale of the rest of it.
+__device__ __forceinline__ unsigned magnitude_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+__device__ __forceinline__ unsigned amax_bits8(const uint4& v) {   // of eight bf16
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    unsigned m = 0u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) m = max(m, max((u[q] << 16) & 0x7FFFFFFFu, u[q] & 0x7FFF0000u));
+    return m;
+}
+
 // The FP8 codes of a row whose largest magnitude is amax: e4m3(x / s) with s = amax / 448, the quotients rounded as
 // IEEE division rounds them: q = RN(x r), r = RN(1 / s), then q + r (x - q s) with the remainder exact in an fma
 // (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).  That needs r
@@ -376,6 +387,7 @@ struct DecodeShared {
     unsigned amax[kDecodeMaxT];
     float sx[kDecodeMaxT];
     float red[2 * (kDecodeWarps + kDecodeStreams) * kDecodeMaxT];
+    unsigned row_max[16 + kDecodeWarps];             // of the multiplying warps' shares of a row of h, for two rows in turn
     int first[4], end[4], per_expert[4];             // this CTA's units of each phase, and how many an expert has
     int need[kDecodeMaxT], n_need;                   // the tokens of this CTA's gate/up experts,
     uint8_t need_at[kDecodeMaxT];                    // and a token's place among them
@@ -845,10 +857,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
 #pragma unroll 2
     for (int b0 = warp * 32; b0 < n_x; b0 += kMul) {
         int tk;
-        float a = amax8(chunk_of(b0 + lane, tk));
+        unsigned a = amax_bits8(chunk_of(b0 + lane, tk));
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        if (tk >= 0 && (lane & 15) == 0) atomicMax(&S.amax[tk], __float_as_uint(a));
+        for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+        if (tk >= 0 && (lane & 15) == 0) atomicMax(&S.amax[tk], a);
     }
     multipliers_sync();
     if (threadIdx.x < T) S.sx[threadIdx.x] = __fdiv_rn(__uint_as_float(S.amax[threadIdx.x]), kFp8Max) * kDecodeLadder<kMx>;
@@ -890,7 +902,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
     for (int q = own_rows ? 0 : cta, odd = 0; q < n_rows; q += own_rows ? 1 : G, odd ^= 16) {   // (the maxima of two rows in turn)
         const int r = own_rows ? S.row_pair[q] : q;
         const float4* src = reinterpret_cast<const float4*>(p.h + (int64_t)r * p.N);
-        float x[8], a = 0.0f;
+        float x[8];
+        unsigned a = 0u;
         auto load = [&](int c) {
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f), w = v;
             if (c < hc) { v = __ldcg(src + 2 * c); w = __ldcg(src + 2 * c + 1); }
@@ -901,12 +914,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
         for (int b0 = 0; b0 < hc; b0 += kMul) {
             load(b0 + threadIdx.x);
 #pragma unroll
-            for (int z = 0; z < 8; ++z) a = fmaxf(a, fabsf(x[z]));
+            for (int z = 0; z < 8; ++z) a = max(a, magnitude_bits(x[z]));
         }
-        a = warp_max(a);
-        if (lane == 0) S.red[warp + odd] = a;
+        a = __reduce_max_sync(0xffffffffu, a);
+        if (lane == 0) S.row_max[warp + odd] = a;
         multipliers_sync();
-        const RowQuant s = RowQuant::of(warp_max(lane < kDecodeWarps ? S.red[lane + odd] : 0.0f));
+        const RowQuant s = RowQuant::of(__uint_as_float(__reduce_max_sync(0xffffffffu, lane < kDecodeWarps ? S.row_max[lane + odd] : 0u)));
 #pragma unroll 1
         for (int b0 = 0; b0 < hc; b0 += kMul) {
             const int c = b0 + threadIdx.x;

@@ -1,0 +1,80 @@
+"""The few-token layer at the ends of its inputs' range."""
+import pytest
+import torch
+
+from conftest import cuda_ok
+from test_decode_gpu import FMT, Case, _dirty_ws
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not cuda_ok():
+        pytest.skip("no CUDA device")
+
+
+@pytest.fixture
+def moe():
+    import bit_quantized_moe_token_b200 as m
+    return m
+
+
+def _run(moe, c, x, routing, k, router):
+    ws = _dirty_ws(moe, c.layer, x.shape[0], k)
+    return (moe.decode_router if router else moe.decode)(c.layer, x, routing, k, ws=ws)
+
+
+# E, H, N, k, T.  The last two have more routed rows of h for one CTA's down units than its shared memory holds, so that
+# the rows go through the workspace.
+NOT_FINITE = [(6, 512, 256, 3, 1), (6, 512, 256, 3, 9), (40, 1152, 640, 2, 4), (3, 640, 384, 3, 16), (2, 256, 8192, 2, 9)]
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("router", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("E,H,N,k,T", NOT_FINITE)
+def test_a_token_that_is_not_finite_has_nan_outputs(moe, fmt, router, bad, E, H, N, k, T):
+    """Without a shared expert: its routed sums are NaN, so its outputs are, and its neighbours' stay bit for bit."""
+    c = Case(moe, fmt, E, H, N, 31 + T)
+    x, lg = c.tokens(T)
+    wr = (torch.randn(E, H, generator=c.g, device="cuda") / H ** 0.5).bfloat16()
+    routing = wr if router else lg
+    want = _run(moe, c, x, routing, k, router)
+    assert torch.isfinite(want).all()
+    t = T // 2
+    x[t, 17] = bad
+    got = _run(moe, c, x, routing, k, router)
+    assert torch.isnan(got[t]).all()
+    rest = [i for i in range(T) if i != t]
+    assert torch.equal(got[rest], want[rest])
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("T", [1, 9])
+def test_a_token_of_zeros_but_one_that_is_not_finite(moe, fmt, bad, T):
+    c = Case(moe, fmt, 6, 512, 256, 32)
+    x, lg = c.tokens(T)
+    x[T - 1] = 0.0
+    x[T - 1, 300] = bad
+    got = moe.decode(c.layer, x, lg, 3, ws=_dirty_ws(moe, c.layer, T, 3))
+    assert torch.isnan(got[T - 1]).all() and torch.isfinite(got[:T - 1]).all()
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("which", [0, 1, 2])
+@pytest.mark.parametrize("E,H,N,T", [(5, 512, 256, 6), (2, 256, 8192, 9)])
+def test_an_expert_whose_scales_are_nan(moe, fmt, which, E, H, N, T):
+    """All scales of one expert's gate, up or down projection: its tokens' outputs are NaN, the others' as they were."""
+    c = Case(moe, fmt, E, H, N, 33)
+    x, lg = c.tokens(T)
+    lg[:, 1] = -5.0
+    lg[::3, 1] = 5.0
+    want = moe.decode(c.layer, x, lg, 1, ws=_dirty_ws(moe, c.layer, T, 1))
+    scales = c.w[which][1]
+    scales[1] = 255 if fmt == "mxfp4" else float("nan")
+    got = moe.decode(c.layer, x, lg, 1, ws=_dirty_ws(moe, c.layer, T, 1))
+    mine = torch.arange(T, device="cuda") % 3 == 0
+    assert torch.isnan(got[mine]).all()
+    assert torch.equal(got[~mine], want[~mine])

@@ -1028,6 +1028,10 @@ inline bool decode_map(CUtensorMap* m, const void* w, uint64_t row_bytes, uint64
     return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, w, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Dynamic shared memory that a CTA may take.  Every launch allows a kernel this much and no call its own size: the
+// allowance is the function's, shared by the host threads, and a smaller layer's call would lower it under another's.
+constexpr size_t kDecodeSmem = 227 * 1024 - sizeof(DecodeShared) - 64;
+
 // How a CTA's 227 KB are divided: the fragments (as f16 for up to six tokens: a CTA's experts seldom have more; room
 // for all as FP8), their group sums, and the warps' rings: chunks of four pieces (8 KB) where two fit, else of two or
 // one.  The rows' scales get buffers beside the slots where they fit, else they are read in place.
@@ -1038,7 +1042,7 @@ struct DecodeSmem {
 
 inline bool plan_decode_smem(const DecodeLayer& L, int64_t T, bool mx, DecodeSmem* out) {
     const int pieces = (L.H + 255) / 256, pieces_h = (L.N + 255) / 256;
-    const size_t room = 227 * 1024 - sizeof(DecodeShared) - 1024 - 64;
+    const size_t room = kDecodeSmem - 1024;   // (the rings start on a 1024-byte boundary)
     const size_t row16 = frag_row_bytes<false>(pieces), row_h = frag_row_bytes<false>(pieces_h);
     const size_t scale = align_up((size_t)16 * std::max(L.H, L.N) / (mx ? 32 : 64), 128);
     for (int in_smem = 1; in_smem >= 0; --in_smem) {
@@ -1064,7 +1068,7 @@ inline bool plan_decode_smem(const DecodeLayer& L, int64_t T, bool mx, DecodeSme
 template <bool kMx, bool kScaleSmem>
 inline int launch_decode(DecodeParams& q, size_t smem, cudaStream_t stream) {
     const void* fn = reinterpret_cast<const void*>(k_decode<kMx, kScaleSmem>);
-    if (set_smem(fn, smem)) return MOE_ERR_CUDA;
+    if (set_smem(fn, kDecodeSmem)) return MOE_ERR_CUDA;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)

@@ -1,4 +1,7 @@
 """The few-token layer at the ends of its inputs' range."""
+import ctypes
+import threading
+
 import pytest
 import torch
 
@@ -78,3 +81,32 @@ def test_an_expert_whose_scales_are_nan(moe, fmt, which, E, H, N, T):
     mine = torch.arange(T, device="cuda") % 3 == 0
     assert torch.isnan(got[mine]).all()
     assert torch.equal(got[~mine], want[~mine])
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_host_threads_with_layers_of_different_sizes(moe, fmt):
+    """Two threads, each with its own stream, workspace and layer, whose kernels take different amounts of shared memory:
+    the C calls at once (ctypes releases the interpreter's lock), as often as it takes them to meet."""
+    call = getattr(moe.lib(), f"moe_{fmt}_decode")
+    statuses, outs, threads = [], [], []
+
+    def loop(struct, args):
+        torch.cuda.set_device(0)
+        statuses.append({call(ctypes.byref(struct), *args) for _ in range(20000)})
+
+    for E, H, N, T in ((2, 128, 128, 1), (2, 1152, 640, 16)):
+        c = Case(moe, fmt, E, H, N, 34)
+        x, lg = c.tokens(T)
+        out, ws, stream = torch.zeros_like(x), _dirty_ws(moe, c.layer, T, 1), torch.cuda.Stream()
+        outs.append((out, moe.decode(c.layer, x, lg, 1), x, lg, ws, stream, c))
+        args = (x.data_ptr(), lg.data_ptr(), T, 1, out.data_ptr(), ws.data_ptr(), ws.nbytes, stream.cuda_stream)
+        threads.append(threading.Thread(target=loop, args=(c.layer.c_struct(), args)))
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert statuses == [{moe.MOE_OK}, {moe.MOE_OK}]
+    for out, want, *_ in outs:
+        assert torch.equal(out, want)

@@ -152,9 +152,10 @@ template <bool kF8>
 __host__ __device__ constexpr uint32_t frag_row_bytes(int pieces) { return pieces * (kF8 ? 256 : 512) + 64; }
 
 constexpr float kNibbleOffset = -8.0f / 16777216.0f;   // -8 2^-24
-// The power of two that the routed products' sums lack.
+// A routed product's sum times a scale.  INT4 sums lack 2^24: it is put back before the scale (exactly), since scale 2^24
+// overflows for rows of 10^34 whose results do not.
 template <bool kMx>
-constexpr float kDecodeLadder = kMx ? 1.0f : 16777216.0f;
+__device__ __forceinline__ float scaled(float acc, float scale) { return (kMx ? acc : acc * 16777216.0f) * scale; }
 
 // A lane's scales (rows g and g + 8) of a piece, from the rows' scales in shared memory (offsets) or, where
 // the buffers do not fit, in place.
@@ -591,11 +592,11 @@ __device__ __forceinline__ void DecodeWarp<kMx, kScaleSmem>::routed() {
                 if (8 * n + col + c1 >= n_tok) continue;
                 const int pr = S.pair[e][8 * n + col + c1];
                 if constexpr (kDown) {
-                    p.y[(int64_t)pr * p.H + b * 16 + r] = acc[n][c1] * S.gs[pr];
-                    p.y[(int64_t)pr * p.H + b * 16 + r + 8] = acc[n][c1 + 2] * S.gs[pr];
+                    p.y[(int64_t)pr * p.H + b * 16 + r] = scaled<kMx>(acc[n][c1], S.gs[pr]);
+                    p.y[(int64_t)pr * p.H + b * 16 + r + 8] = scaled<kMx>(acc[n][c1 + 2], S.gs[pr]);
                 } else {
                     const float sx = S.sx[S.list[e][8 * n + col + c1]];
-                    p.h[(int64_t)pr * p.N + b * 8 + r] = silu(acc[n][c1] * sx) * (acc[n][c1 + 2] * sx);
+                    p.h[(int64_t)pr * p.N + b * 8 + r] = silu(scaled<kMx>(acc[n][c1], sx)) * scaled<kMx>(acc[n][c1 + 2], sx);
                 }
             }
     }
@@ -863,7 +864,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
         if (tk >= 0 && (lane & 15) == 0) atomicMax(&S.amax[tk], a);
     }
     multipliers_sync();
-    if (threadIdx.x < T) S.sx[threadIdx.x] = __fdiv_rn(__uint_as_float(S.amax[threadIdx.x]), kFp8Max) * kDecodeLadder<kMx>;
+    if (threadIdx.x < T) S.sx[threadIdx.x] = __fdiv_rn(__uint_as_float(S.amax[threadIdx.x]), kFp8Max);
 #pragma unroll 1
     for (int b0 = warp * 32; b0 < n_x; b0 += kMul) {
         int tk;
@@ -936,7 +937,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const __grid_const
                 if (c < hc && (lane & 15) == 0) to[c >> 4] = sum;
             }
         }
-        if (threadIdx.x == 0) (own_rows ? S.gs : p.gs)[r] = S.gates[r] * s.s * kDecodeLadder<kMx>;
+        if (threadIdx.x == 0) (own_rows ? S.gs : p.gs)[r] = S.gates[r] * s.s;
     }
     if (own_rows) {
         multipliers_sync();

@@ -544,7 +544,9 @@ typedef struct {
  *   G[n] = s_x[t] * sum_b 2^(b8_gate[e,n,b] - 127) * sum_{k in b} Xq[t,k] * C_gate[e,n,k]   (likewise U)
  * and Y from Hq in the same way.  Sums are fp32 in an order of the kernel's own (the same on every
  * call), so outputs agree with moe_w4a8_forward to rounding, not bit for bit.  A token that holds a
- * NaN or an infinity, or a row of whose h does, has NaN outputs; no other token's change.  The _router forms
+ * NaN or an infinity, or a row of whose h does, has NaN outputs; no other token's change.  W4A8 group
+ * scales below 2^-100 (and not 0) lose precision: the sums before 2^24 is put back leave fp32's normal
+ * range.  The _router forms
  * compute the logits from the router weight (moe_router_logits' definition).
  *
  *   x_bf16 [T, H]   router_logits [T, E] fp32 or wr_bf16 [E, H]   out_bf16 [T, H] (may be x_bf16)

@@ -110,3 +110,30 @@ def test_host_threads_with_layers_of_different_sizes(moe, fmt):
     assert statuses == [{moe.MOE_OK}, {moe.MOE_OK}]
     for out, want, *_ in outs:
         assert torch.equal(out, want)
+
+
+def _scale_by(c, which, power):
+    """The projection's scales times 2^power."""
+    scales = c.w[which][1]
+    if c.fmt == "mxfp4":
+        scales += power
+    else:
+        scales *= 2.0 ** power
+
+
+# x and the gate and up scales times powers of two: g and u stay near 2^56, h near 2^112
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("x_power,w_power", [(0, 56), (113, -57), (-100, 100)])
+@pytest.mark.parametrize("E,H,N,k,T", [(6, 512, 256, 2, 1), (6, 512, 256, 2, 9), (2, 256, 2048, 1, 16)])
+def test_large_and_small_values_that_cancel(moe, fmt, x_power, w_power, E, H, N, k, T):
+    """Tokens, and rows of h, near the ends of fp32's range: outputs that bf16 holds come out as such."""
+    if x_power == -100:
+        w_power -= 44 if fmt == "mxfp4" else 40   # g and u near 2^-40
+    c = Case(moe, fmt, E, H, N, 35 + T)
+    x, lg = c.tokens(T)
+    x *= 2.0 ** x_power
+    for which in (0, 1):
+        _scale_by(c, which, w_power)
+    out = moe.decode(c.layer, x, lg, k, ws=_dirty_ws(moe, c.layer, T, k))
+    assert torch.isfinite(out).all()
+    c.check(out, x, lg, k)

@@ -1,6 +1,8 @@
 """Convenience wrappers: torch allocation around the C entry points."""
 from __future__ import annotations
 
+import math
+
 from ._binding import (Layer, Layer4, Layer8, LayerH, LayerMX, moe_hybrid_forward, moe_hybrid_workspace_bytes,
                        moe_mxfp4_decode, moe_mxfp4_decode_router, moe_mxfp4_decode_workspace_bytes,
                        moe_nvfp4_forward, moe_nvfp4_workspace_bytes,
@@ -148,8 +150,9 @@ def quant_mxfp4(x, stream=None):
             return quant_mxfp4(x)
     import torch
     if x.dim() != 2:
-        codes, scales = quant_mxfp4(x.reshape(-1, x.shape[-1]))
-        return codes.view(*x.shape[:-1], -1), scales.view(*x.shape[:-1], -1)
+        *lead, K = x.shape
+        codes, scales = quant_mxfp4(x.reshape(math.prod(lead), K))
+        return codes.view(*lead, K // 2), scales.view(*lead, K // 32)
     rows, K = x.shape
     if K % 32:
         raise ValueError("K must be a multiple of 32")
@@ -167,8 +170,11 @@ def dequant_mxfp4(codes, scales, dtype=None, stream=None):
             return dequant_mxfp4(codes, scales, dtype)
     import torch
     if codes.dim() != 2:
-        y = dequant_mxfp4(codes.reshape(-1, codes.shape[-1]), scales.reshape(-1, scales.shape[-1]), dtype)
-        return y.view(*codes.shape[:-1], -1)
+        *lead, half = codes.shape
+        if tuple(scales.shape) != (*lead, half // 16):
+            raise ValueError(f"scales: expected {[*lead, half // 16]}, got {list(scales.shape)}")
+        y = dequant_mxfp4(codes.reshape(math.prod(lead), half), scales.reshape(math.prod(lead), half // 16), dtype)
+        return y.view(*lead, 2 * half)
     y = codes.new_empty((codes.shape[0], 2 * codes.shape[1]), dtype=dtype or torch.bfloat16)
     mxfp4_dequant_rows(codes, scales, y)
     return y

@@ -816,6 +816,9 @@ def _weights(dev, E, H, N, gate, up, down, dtype, per):
 
 
 def _decode(name: str, layer, x, routing, router: bool, k: int, out, ws, stream):
+    kind = Layer if name == "w4a8" else LayerMX
+    if not isinstance(layer, kind):
+        raise ValueError(f"moe_{name}_decode: expected a {kind.__name__}, got {type(layer).__name__}")
     torch, L, _ = _entry()
     dev, bf16 = torch._C._cuda_getDevice(), torch.bfloat16
     E, H, N, T = layer.E, layer.H, layer.N, x.shape[0]

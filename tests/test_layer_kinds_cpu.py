@@ -1,0 +1,40 @@
+"""Each layer call refuses the expert formats that it does not compute, by name and before anything else."""
+import pytest
+
+import bit_quantized_moe_token_b200 as moe
+
+W = [None] * 6
+W4, F8, F4, MX = (moe.Layer(8, 256, 128, *W), moe.Layer8(8, 256, 128, *W), moe.Layer4(8, 256, 128, *W, *W[:3]),
+                  moe.LayerMX(8, 256, 128, *W))
+HYBRID = moe.LayerH(8, F4, W4, None, None)
+
+
+@pytest.mark.parametrize("layer", [MX, None])
+def test_forward(layer):
+    for call in (lambda: moe.forward(layer, None, None, 2), lambda: moe.forward(layer, None, None, 2, out=0, ws=0),
+                 lambda: moe.alloc_workspace(layer, 4, 2, "cpu")):
+        with pytest.raises(ValueError, match="forward: expected a layer of type Layer or Layer8 or Layer4 or LayerH"):
+            call()
+
+
+@pytest.mark.parametrize("layer", [F8, F4, HYBRID, None])
+def test_few_token_layer(layer):
+    for call in (lambda: moe.decode(layer, None, None, 2), lambda: moe.decode(layer, None, None, 2, out=0, ws=0),
+                 lambda: moe.decode_router(layer, None, None, 2, out=0, ws=0),
+                 lambda: moe.alloc_decode_workspace(layer, 4, 2, "cpu")):
+        with pytest.raises(ValueError, match="decode(_router)?: expected a layer of type Layer or LayerMX"):
+            call()
+
+
+@pytest.mark.parametrize("fmt,layer", [("w4a8", MX), ("w4a8", F8), ("mxfp4", W4), ("mxfp4", F4)])
+def test_entry_points(fmt, layer):
+    for tail in ("decode", "decode_router"):
+        with pytest.raises(ValueError, match=f"moe_{fmt}_decode: expected a"):
+            getattr(moe, f"moe_{fmt}_{tail}")(layer, None, None, 2, None, None)
+
+
+def test_the_formats_that_are_computed_get_their_workspace():
+    for layer in (W4, F8, F4):
+        assert moe.alloc_workspace(layer, 4, 2, "cpu").numel() > 0
+    for layer in (W4, MX):
+        assert moe.alloc_decode_workspace(layer, 4, 2, "cpu").numel() > 0

@@ -271,8 +271,13 @@ __device__ __forceinline__ uint32_t in_first(uint64_t* bar) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(tc::smem_u32(bar)));
     return a;
 }
+// What a warp of the second CTA hands to the thread that issues the MMAs for both lies in TMEM (its scales stored there, its
+// part of the accumulator read): tcgen05.wait and the tcgen05 fences around arrival and wait order it.  The arrival
+// therefore needs the cluster's scope but no release of memory (with release.cluster, which waits for the warp's stores,
+// 16384 x 4096 x 4096 takes 214 us against 112).  That thread waits at the same scope, from which the bytes of the other
+// CTA's TMA loads come too.
 __device__ __forceinline__ void arrive_first(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_first(bar)) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_first(bar)) : "memory");
 }
 // A TMA load into this CTA's shared memory whose bytes count on the first CTA's barrier.
 __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
@@ -366,10 +371,10 @@ __global__ void __launch_bounds__(Cfg<BN, kPair>::kThreads, 1) k_gemm(const __gr
             ws::Ring<C::kStages> r;
             uint32_t phase = 0;
             for (int tile = tile0; ok && tile < tiles; tile += tile_step, phase ^= 1u) {
-                ok = ws::wait(&acc_empty, phase ^ 1u, &abort);
+                ok = ws::wait<kPair>(&acc_empty, phase ^ 1u, &abort);
                 tc::tc_fence_after();
                 for (int s = 0; ok && s < stages; ++s, r.next()) {
-                    ok = ws::wait(&full[r.idx], r.phase, &abort);
+                    ok = ws::wait<kPair>(&full[r.idx], r.phase, &abort);
                     if (!ok) break;
                     tc::tc_fence_after();
                     const uint32_t a = base + r.idx * C::kStage, sf = tmem + kScaleCol + r.idx * C::kCols;

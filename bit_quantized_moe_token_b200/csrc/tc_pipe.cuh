@@ -53,11 +53,12 @@ struct Ring {
     }
 };
 
-// Bounded wait that gives up at once after an abort.
+// Bounded wait that gives up at once after an abort (kCluster: see mbar_try_wait).
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    if (tc::mbar_try_wait(bar, parity)) return true;      // completed phase: no flag read
+    if (tc::mbar_try_wait<kCluster>(bar, parity)) return true;      // completed phase: no flag read
     if (*abort) return false;
-    if (tc::mbar_wait(bar, parity)) return true;
+    if (tc::mbar_wait<kCluster>(bar, parity)) return true;
     *abort = 1;
     return false;
 }

@@ -34,10 +34,27 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
 
 // One potentially blocking test of the phase: with a suspend-time hint the thread sleeps until
 // the phase completes (or about `hint_ns` pass) instead of spinning and taking issue slots
-// from the warps that do the work.
+// from the warps that do the work.  kCluster: at the cluster's scope, for barriers on which other CTAs arrive too.
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity, uint32_t hint_ns = 0) {
     uint32_t ok;
-    if (hint_ns) {
+    if (kCluster && hint_ns) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
+            : "memory");
+    } else if (kCluster) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+    } else if (hint_ns) {
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
             "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
@@ -65,12 +82,13 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 
 // Wait for the phase with the given parity to complete, giving up after `limit_ns` of wall
 // time (default 2 s).  Returns false when the bound ran out.
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
                                           uint64_t limit_ns = 2000000000ull) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait<kCluster>(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
-        if (mbar_try_wait(bar, parity, 200000u)) return true;     // sleeps up to ~0.2 ms per try
+        if (mbar_try_wait<kCluster>(bar, parity, 200000u)) return true;     // sleeps up to ~0.2 ms per try
         if (globaltimer_ns() - t0 > limit_ns) return false;
     }
 }

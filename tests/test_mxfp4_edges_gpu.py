@@ -1,4 +1,4 @@
-"""MXFP4 rows in tensors of other ranks than two, empty ones among them."""
+"""MXFP4 rows in tensors of other ranks than two, empty ones among them, and the product by pairs of CTAs."""
 import pytest
 import torch
 
@@ -46,3 +46,29 @@ def test_scales_of_other_rows_are_refused(moe, shape):
     codes, _ = moe.quant_mxfp4(torch.zeros(2, 3, 96, device="cuda", dtype=torch.bfloat16))
     with pytest.raises(ValueError):
         moe.dequant_mxfp4(codes, torch.full(shape, 127, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("M,N,K,dtype", [(2304, 2560, 512, torch.bfloat16), (2500, 2300, 1056, torch.float32), (4097, 2600, 288, torch.bfloat16)])
+def test_pairs_of_ctas_repeat_bit_for_bit(moe, M, N, K, dtype):
+    """Sizes that pairs of CTAs compute (with the scales by TMA and by loads), many products of changing operands in a
+    row: what the second CTA hands to the first is there before it is used."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M)
+
+    def rows(R):
+        return (torch.randint(0, 256, (R, K // 2), generator=g, device="cuda", dtype=torch.uint8),
+                torch.randint(118, 123, (R, K // 32), generator=g, device="cuda", dtype=torch.uint8))
+
+    sets = [(rows(M), rows(N)) for _ in range(3)]
+    want = []
+    for (a, sa), (b, sb) in sets:
+        va, vb = plain64.mxfp4_values(a, sa), plain64.mxfp4_values(b, sb)
+        ref = va @ vb.T
+        want.append(moe.matmul_mxfp4(a, sa, b, sb, dtype=dtype))
+        assert ((want[-1].double() - ref).abs() <= plain64.matmul_tolerance(va, vb, ref, dtype)).all()
+    outs = [torch.empty_like(want[0]) for _ in range(3)]
+    for _ in range(50):
+        for ((a, sa), (b, sb)), out, first in zip(sets, outs, want):
+            moe.matmul_mxfp4(a, sa, b, sb, out=out)
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    assert moe.moe_last_device_status() == 0

@@ -339,10 +339,13 @@ __device__ __forceinline__ unsigned amax_bits8(const uint4& v) {   // of eight b
     return m;
 }
 
-// The FP8 codes of a row whose largest magnitude is amax: e4m3(x / s) with s = amax / 448, the quotients rounded as
-// IEEE division rounds them: q = RN(x r), r = RN(1 / s), then q + r (x - q s) with the remainder exact in an fma
-// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).  That needs r
-// normal and remainders that do not underflow where they matter; rows outside [2^-60, 2^60] divide plainly.
+// The FP8 codes of a row whose largest magnitude is amax: e4m3(x / s) with s = amax / 448, by r = RN(1 / s), q = RN(x r) and
+// q + r (x - q s) with the remainder in a fused multiply-add (the correction of P. Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990).  q is off by up to 1.5 units in its last place, more than the
+// theorem there allows, but the corrected quotient is within 2^-21 of one before it is rounded, so a code could differ from
+// that of IEEE division only where x / s lies that near to the middle of two floats beside a tie of two codes; of all
+// mantissas of x and s 255 pairs do, and every one of them is rounded right (tests/test_decode_division_cpu.py).  The method
+// needs r normal and remainders that do not underflow where they matter; rows outside [2^-60, 2^60] divide plainly.
 struct RowQuant {
     float s, r;
     bool plain;

@@ -137,3 +137,59 @@ def test_large_and_small_values_that_cancel(moe, fmt, x_power, w_power, E, H, N,
     out = moe.decode(c.layer, x, lg, k, ws=_dirty_ws(moe, c.layer, T, k))
     assert torch.isfinite(out).all()
     c.check(out, x, lg, k)
+
+
+def _identity(fmt, rows, K, columns):
+    """Weights [1, rows, K] with a one in column columns[n] of row n."""
+    w = torch.zeros(1, rows, K, device="cuda", dtype=torch.int64)
+    w[0, torch.arange(rows, device="cuda"), columns] = 1
+    if fmt == "mxfp4":     # E2M1 code 2 is 1, E8M0 scale 127 is 1
+        codes = (2 * w).unflatten(-1, (-1, 2))
+        return ((codes[..., 0] + 16 * codes[..., 1]).to(torch.uint8),
+                torch.full((1, rows, K // 32), 127, dtype=torch.uint8, device="cuda"))
+    n = (w + 8).unflatten(-1, (-1, 8))
+    packed = (n << torch.arange(0, 32, 4, device="cuda")).sum(-1)
+    packed = torch.where(packed >= 2 ** 31, packed - 2 ** 32, packed).int()
+    return packed, torch.ones(1, rows, K // 128, dtype=torch.bfloat16, device="cuda")
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("T", [4, 16])
+def test_tokens_codes_are_those_of_ieee_division(moe, fmt, T):
+    """Every quotient of bf16 numbers that a token's quantization meets, x / (amax / 448): 128 mantissas of amax (a token
+    each) by 128 mantissas and 18 exponents of x (the columns), as f16 (T = 4) and FP8 (T = 16) fragments.
+
+    The layer reads them out: one expert, whose gate rows all take the column of amax (so that silu(g) is one positive
+    number), its up row n column n, its down row n h[n].  h[n] is then proportional to code[n], so is its FP8 code, and
+    out[n] / out[at amax] = code[n] / 448 to bf16's rounding, 2^-7 in all: neighbouring codes differ by 2^-4 or more.
+
+    W4A8 sums codes times nibbles n = 8 (a zero) or 9 onto -8 sum q, in fp32: with S the sum of a group's |q|, no partial
+    sum exceeds 8 S + 9 S, and each of the group's some 20 additions (16 MMAs in chains, which may truncate, and the joins) is
+    off by at most 2^-23 of that, so a code read out is off by 20 17 2^-23 S."""
+    H = 128 * 18
+    mantissa = torch.arange(128, 256, device="cuda").double() / 128
+    x = (mantissa[:, None] * 2.0 ** -torch.arange(18, device="cuda").double()).flatten()      # column c: 2^-(c % 18)
+    top = H - 1
+    cols = torch.arange(H, device="cuda")
+    gate, up = _identity(fmt, H, H, torch.full_like(cols, top)), _identity(fmt, H, H, cols)
+    kind = moe.Layer if fmt == "w4a8" else moe.LayerMX
+    layer = kind(1, H, H, gate[0], up[0], up[0], gate[1], up[1], up[1])
+    lg = torch.zeros(T, 1, device="cuda")
+    ws = moe.alloc_decode_workspace(layer, T, 1)
+    for first in range(0, 128, T):
+        amax = mantissa[first:first + T]
+        tokens = x.repeat(T, 1)
+        tokens = torch.where(tokens > amax[:, None], tokens / 2, tokens)
+        tokens[:, 1::2] *= -1
+        tokens[:, top] = amax
+        tokens = tokens.bfloat16()
+        out = moe.decode(layer, tokens, lg, 1, ws=ws).double()
+        scale = amax.float() / torch.full_like(amax, 448).float()
+        want = (tokens.float() / scale[:, None]).to(torch.float8_e4m3fn).double()
+        got = out / out[:, top:] * 448
+        assert (want[:, top] == 448).all()
+        tol = 2.0 ** -6 * want.abs()
+        if fmt == "w4a8":
+            groups = want.abs().unflatten(1, (-1, 128)).sum(2)
+            tol += 20 * 17 * 2.0 ** -23 * groups.repeat_interleave(128, 1)
+        assert ((got - want).abs() <= tol).all()

@@ -257,6 +257,8 @@ inline size_t route_ws_bytes(int64_t T, int E, int k) {
     return align_up(static_cast<size_t>(nchunks > 0 ? nchunks : 1) * E * sizeof(int32_t), 256);
 }
 
+// Allows a kernel `bytes` of dynamic shared memory.  The allowance is the function's, shared by all host threads, so callers
+// give the most that any launch takes, not their own size: a smaller one would refuse another thread's larger launch.
 inline int set_smem(const void* fn, size_t bytes) {
     if (bytes <= 48 * 1024) return MOE_OK;
     return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -270,7 +272,7 @@ inline int launch_permute(const int32_t* ids, int64_t T, int E, int k, int32_t* 
     const int64_t P = T * k;
     if (P <= kSinglePassMaxP) {
         const size_t smem = permute_block_smem(E);
-        if (set_smem((const void*)k_permute_single, smem)) return MOE_ERR_CUDA;
+        if (set_smem((const void*)k_permute_single, permute_block_smem(kMaxE))) return MOE_ERR_CUDA;
         return launch_pdl(k_permute_single, dim3(1), dim3(1024), smem, stream, ids, P, E, offsets, sorted, rop, zero,
                           n_zero);
     }
@@ -283,7 +285,7 @@ inline int launch_permute(const int32_t* ids, int64_t T, int E, int k, int32_t* 
         st = launch_pdl(k_chunk_scan, dim3(1), dim3(1024), (2 * E + 33) * sizeof(int), stream, counts, nchunks, P, E,
                         offsets);
     const size_t smem = (E + 32 * E) * sizeof(int);
-    if (st == MOE_OK && set_smem((const void*)k_chunk_scatter, smem)) return MOE_ERR_CUDA;
+    if (st == MOE_OK && set_smem((const void*)k_chunk_scatter, (kMaxE + 32 * kMaxE) * sizeof(int))) return MOE_ERR_CUDA;
     if (st == MOE_OK)
         st = launch_pdl(k_chunk_scatter, dim3(static_cast<unsigned>(nchunks)), dim3(1024), smem, stream, ids, P, E,
                         counts, sorted, rop);

@@ -184,14 +184,12 @@ int launch_router_gemv(const uint16_t* x, const uint16_t* wr, int64_t T, int H, 
                        unsigned* counters = nullptr) {
     const size_t smem = static_cast<size_t>(kTB) * H * 2;
     auto kern = k_router_gemv<kTB, kTopk, EPL>;
-    static int smem_set[16] = {0};                   // per device: the largest opt-in so far
+    static bool allowed[16] = {};   // per device; the same for every H (kTB H <= 64 K), so that no call lowers another's
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
-    if (smem > 48 * 1024 && static_cast<int>(smem) > smem_set[dev & 15]) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-            cudaSuccess)
-            return MOE_ERR_CUDA;
-        smem_set[dev & 15] = static_cast<int>(smem);
+    if (!allowed[dev & 15]) {
+        if (set_smem(reinterpret_cast<const void*>(kern), 128 * 1024) != MOE_OK) return MOE_ERR_CUDA;
+        allowed[dev & 15] = true;
     }
     const dim3 grid(static_cast<unsigned>((E + 7) / 8), static_cast<unsigned>((T + kTB - 1) / kTB));
     return launch_pdl(kern, grid, dim3(256), smem, stream, reinterpret_cast<const uint4*>(x),

@@ -53,3 +53,34 @@ def test_two_threads(T):
         assert torch.equal(sorted_pairs.long(), want.sort(stable=True).indices)
         assert torch.equal(rows[sorted_pairs.long()].long(), torch.arange(T * k, device="cuda"))
         assert offsets[-1] == T * k
+
+
+def test_router_weights_of_two_widths():
+    """The router's logits from two threads, H = 2048 and 4096: 64 and 128 KB of tokens in shared memory."""
+    import bit_quantized_moe_token_b200 as moe
+    call = moe.lib().moe_router_logits
+    statuses, sets, threads = [], [], []
+
+    def loop(args):
+        torch.cuda.set_device(0)
+        statuses.append({call(*args) for _ in range(5000)})
+
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    for H in (2048, 4096):
+        x, wr = ((torch.randn(n, H, generator=g, device="cuda")).bfloat16() for n in (40, 60))
+        out = torch.empty(40, 60, device="cuda")
+        stream = torch.cuda.Stream()
+        sets.append((x, wr, out, stream))
+        threads.append(threading.Thread(target=loop, args=((x.data_ptr(), wr.data_ptr(), 40, H, 60, out.data_ptr(), stream.cuda_stream),)))
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert statuses == [{moe.MOE_OK}, {moe.MOE_OK}]
+    for x, wr, out, _ in sets:
+        ref = x.double() @ wr.double().T
+        # an fp32 sum of H terms in any order
+        assert ((out.double() - ref).abs() <= x.shape[1] * 2.0 ** -24 * (x.double().abs() @ wr.double().abs().T)).all()

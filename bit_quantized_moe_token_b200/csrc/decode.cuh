@@ -25,8 +25,9 @@
 // pieces of 16 rows x 128 bytes in the 128-byte swizzle, one TMA box a row set), so that no warp waits for another's data;
 // a streaming warp has a lane for each ring it feeds.  Issued by the multiplying warps themselves a chunk's copies cost
 // them some 1,000 cycles.  A row's scales come beside its unit's first chunk where the buffers fit, else they are read in
-// place.  Measured, in us for W4A8 (T = 1, 8 and 16) and MXFP4 (T = 1 and 8) at the sizes below:
-//   8 + 4 warps                          38.8  137  285   41  138
+// place.  Measured against each other on one build, in us for W4A8 (T = 1, 8 and 16) and MXFP4 (T = 1 and 8) at the sizes
+// below, the same inputs over and over:
+//   8 + 4 warps                          37.8  137  285   41  138
 //   12 + 4 (chunks of two pieces)        36.9  146  336   40  146
 //   9 + 3                                40.3  143  333   44  154
 //   10 + 2                               39.6  145  339   44  163
@@ -40,20 +41,29 @@
 // f16, and so are the weights:
 //   INT4:  a nibble n = code + 8 left where it lies in a 16-bit half is the f16 subnormal n 2^-24 (bits 0..3) or n 2^-20
 //          (bits 4..7, whose tokens' values carry 2^-4), so widening a packed word costs four ANDs and a shift; the
-//          accumulator starts at -8 2^-24 sum q, which takes the offset off again.
+//          accumulator starts at -8 2^-24 sum q, which takes the offset off again.  A group's fp32 sum thus runs over
+//          numbers of up to 23 sum |q|, where the result has 8 sum |q| at most: it is exact while 23 sum |q| < 2^15 (codes
+//          are multiples of 2^-9), and beyond that loses the last bits of the group's smallest codes.
 //   MXFP4: cvt.rn.f16x2.e2m1x2.
 // (mma.sync on E4M3 is no way round the conversion: with it the layer at T = 8 took 213 us.)  A group's (block's) partial
 // sum is scaled in fp32 by its weight scale: one promotion every 128 (32) weights.  Shared experts run on the bf16 MMA,
 // their activation as bf16 hi + lo halves (16 bits of it).
 //
-// Measured, E = 256, top 6, H = 4096, N = 2048: W4A8 T = 1 38.8 us (78 MB: 31 % of HBM's measured 6.56 TB/s), T = 8 with
-// the router 137 us (578 MB: 64 %), T = 16 with two shared experts 285 us (1.15 GB: 61 %); MXFP4 T = 1 with the router
-// 41 us (31 %), T = 8 138 us (593 MB: 66 %).  At T = 1 the chain is: lists 4.6 us, tokens quantized 9.5, gate/up 22,
-// barrier 24, h quantized 26, down 32, sums 34.  At T = 8 the same grid reads the bytes in 104 us when nothing is
-// multiplied, and the multiplying warps find their chunks there (they wait 5 % of the gate/up phase): what they are short
-// of is issue slots.  A piece is some 200 warp instructions (80 of them the widening's half-rate logic) in 640 cycles, two
-// warps a scheduler.  Loading half a piece ahead of the MMAs (147 us), or addresses that run from piece to piece (145),
-// hide latency but add instructions.
+// Measured, E = 256, top 6, H = 4096, N = 2048, each call with other tokens and experts (16 calls or more touch all 3.3 GB):
+// W4A8 from logits
+//   T                                 1     2     4     8    12    16
+//   us                             38.3  53.4  83.0   136   183   227      (78 MB at T = 1: 31 % of HBM's measured 6.56 TB/s;
+//   moe_w4a8_forward               46.5  64.9  92.9   147   194   238       578 MB at T = 8: 65 %)
+//   with two shared experts        64.3  79.3   107   160   242   286
+//   moe_w4a8_forward                143   160   193   244   293   314
+// and MXFP4 38.6, 55.2, 83.6, 138, 185 and 257.  The router form takes 2 to 5 us more.  With the same six experts in every
+// call, which L2 then holds, T = 1 takes 34 to 36 us.  The gain over the forward shrinks with T, hence 16.
+// At T = 1 the chain is: lists 4.6 us, tokens quantized 9.5, gate/up 22, barrier 24, h quantized 26, down 32, sums 34.  At
+// T = 8 the same grid reads the bytes in 104 us when nothing is multiplied, and the multiplying warps find their chunks
+// there (they wait 5 % of the gate/up phase).  A piece is some 200 warp instructions (80 of them the widening's half-rate
+// logic) in 640 cycles, two warps a scheduler; no unit is saturated (issue slots 42 % and ALU 41 % of the whole kernel), so
+// what is left are the fixed latencies of the widening and the MMAs, which two warps do not cover.  Loading half a piece
+// ahead of the MMAs (147 us), or addresses that run from piece to piece (145), hide latency but add instructions.
 #pragma once
 #include <cooperative_groups.h>
 #include <type_traits>

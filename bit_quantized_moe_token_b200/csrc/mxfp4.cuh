@@ -15,8 +15,8 @@
 // through two shuffles.  A thread has four such chunks in flight.
 //
 // Measured: 16384 x 4096 bf16 quantized and read back in 57 us (340 MB: 91 % of HBM's measured 6.56
-// TB/s; with one chunk a thread 80 us); 1000 x 4128 fp32 rows of a wider buffer in 6.9 us, 8 x 4096
-// in 3.4: two launches, which is what a few rows cost.
+// TB/s; with one chunk a thread 80 us); 1000 x 4128 fp32 rows of a wider buffer in 6.8 us, 8 x 4096
+// in 3.4: two launches, which is what a few rows cost (the same inputs over and over, so from L2).
 #pragma once
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>

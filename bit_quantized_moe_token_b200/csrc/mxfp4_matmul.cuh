@@ -16,12 +16,15 @@ namespace moe {
 // MMA pair covers one block; E2M1 is exact in f16.  A block's sum is a multiple of 1/4 below 2^11: multiplied first by
 // the smaller of its two scales it neither overflows (unless the result does) nor loses bits, and a scale of 255 (NaN,
 // the largest as bits too) stays what it is.
-// Measured (bf16 out): 4096 x 4096 weights at M = 1 6.2 us (8.9 MB: 22 % of HBM's measured rate, a chain of latencies), at
-// M = 8 7.7.  It serves one wave of CTAs, two an SM for up to eight tokens and one beyond; more rows of B, and M > 16, go
-// to the tensor-memory kernel, which reads 128 rows of A whatever M is.  This kernel against that one, in us:
-//   M = 1, 4096 x 4096  6.2 10.3    M = 8, 4096 x 4096  7.7 10.3    M = 16, 2048 x 4096  6.2  9.2
-//          8192 x 4096 10.8 12.4           8192 x 4096 13.4 12.4            4096 x 4096 11.3 10.5
-//         14336 x 4096 18.1 13.9          14336 x 4096 22.1 14.3           14336 x 4096 38.5 14.7
+// Measured (bf16 out, M = 1, 4096 x 4096 weights, 8.9 MB): 6.9 us with weights that come from HBM (20 % of its measured rate,
+// a chain of latencies), 6.1 with the same weights, then in L2, in every call.  It serves one wave of CTAs, two an SM for up
+// to eight tokens and one beyond; more rows of B, and M > 16, go to the tensor-memory kernel, which reads 128 rows of A
+// whatever M is.  This kernel against that one, in us, weights from HBM (in L2):
+//            2048 x 4096              4096 x 4096               8192 x 4096                14336 x 4096
+//   M =  1   4.3 (3.6)  9.2 (8.7)     6.9 (6.1)  10.6 (10.1)    11.5 (10.2)  11.6 (10.7)   18.3 (16.6)  14.5 (13.3)
+//   M =  8   5.3 (4.5)  9.2 (8.7)     8.0 (7.2)  10.7 (10.1)    13.7 (13.1)  12.2 (11.6)   21.9 (20.1)  14.3 (13.1)
+//   M = 16   6.8 (5.9)  9.2 (8.8)    12.1 (11.0) 10.4 ( 9.6)    22.7 (20.8)  12.0 (11.3)   38.2 (35.2)  13.8 (13.0)
+// (The rule gives away up to half a microsecond at M = 1 and 8192 rows, where the two meet.)
 namespace mxmm {
 
 // Sixteen scales (blocks b .. b + 15) of a row of `blocks`; 0 past its end.  One 16-byte load where the row allows it:
@@ -158,10 +161,12 @@ __global__ void __launch_bounds__(256) k_few(const uint8_t* __restrict__ a, cons
 //
 // The accumulator's 256 columns and the scales leave no room in TMEM for a second one, so the draining warps first take it
 // into registers (rounded to the output type), free it, and store while the next tile's MMAs run: sixteen warps of 64
-// columns, whose registers suffice without spills (eight of 128: 144 us against 136).
+// columns (eight of 128: 144 us against 136), which leaves 80 registers a thread; 4 bytes a thread are spilled for bf16
+// outputs and 40 for fp32.
 //
-// Measured (bf16 out): 16384 x 4096 x 4096 115 us = 4,770 TFLOP/s, 2.85 times the measured bf16 peak (FP4's nominal rate
-// is four times bf16's); K = 8192 5,170 TFLOP/s; 2048 x 4096 x 4096 19.2 us: two waves for 1.73 waves of tiles.
+// Measured (bf16 out): 16384 x 4096 x 4096 111 to 115 us in runs of six products, 4,800 to 4,970 TFLOP/s, some 2.9 times the
+// measured bf16 peak (FP4's nominal rate is four times bf16's); one call after another for longer, under the power limit,
+// 136 to 140 us = 3,900 to 4,040 TFLOP/s.  2048 x 4096 x 4096 19.9 us: two waves for 1.73 waves of tiles.
 namespace mxmm {
 
 constexpr int kStageK = 256;

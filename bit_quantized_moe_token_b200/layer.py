@@ -191,7 +191,9 @@ def dequant_mxfp4(codes, scales, dtype=None, stream=None):
 
 
 def matmul_mxfp4(a, a_scales, b, b_scales, dtype=None, out=None, stream=None):
-    """A B^T [M, N] of MXFP4 rows A [M, K] and B [N, K], as bf16 (the default) or fp32."""
+    """A B^T [M, N] of MXFP4 rows A [M, K] and B [N, K], as bf16 (the default) or fp32; into `out`, of its type, if given."""
+    if out is not None and dtype is not None and out.dtype != dtype:
+        raise ValueError(f"dtype {dtype}, but out is {out.dtype}")
     if stream is not None:
         with _on(stream):
             return matmul_mxfp4(a, a_scales, b, b_scales, dtype, out)

@@ -1,5 +1,6 @@
 """Each layer call refuses the expert formats that it does not compute, by name and before anything else."""
 import pytest
+import torch
 
 import bit_quantized_moe_token_b200 as moe
 
@@ -38,3 +39,9 @@ def test_the_formats_that_are_computed_get_their_workspace():
         assert moe.alloc_workspace(layer, 4, 2, "cpu").numel() > 0
     for layer in (W4, MX):
         assert moe.alloc_decode_workspace(layer, 4, 2, "cpu").numel() > 0
+
+
+def test_product_of_one_type_into_another():
+    out = torch.empty(2, 2, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="but out is"):
+        moe.matmul_mxfp4(None, None, None, None, dtype=torch.float32, out=out)

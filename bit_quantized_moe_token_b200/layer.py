@@ -99,16 +99,19 @@ def hybrid_from(w4: Layer, f4: Layer4, hot_ids) -> LayerH:
     return LayerH(w4.E, h, c, hot.contiguous(), cold.contiguous())
 
 
-def _takes(layer, kinds, call: str):
-    """Refuses a layer of another format than the call computes."""
-    if not isinstance(layer, kinds):
-        names = " or ".join(kind.__name__ for kind in kinds)
-        raise ValueError(f"{call}: expected a layer of type {names}, got {type(layer).__name__}")
+def _not_mxfp4(layer):
+    if isinstance(layer, LayerMX):
+        raise ValueError("forward: expected a layer of type Layer or Layer8 or Layer4 or LayerH, got LayerMX, which is decode's")
+
+
+def _few_token(layer, call: str):
+    if not isinstance(layer, (Layer, LayerMX)):
+        raise ValueError(f"{call}: expected a layer of type Layer or LayerMX, got {type(layer).__name__}")
 
 
 def alloc_workspace(layer, T: int, k: int, device=None):
     import torch
-    _takes(layer, (Layer, Layer8, Layer4, LayerH), "forward")
+    _not_mxfp4(layer)
     if isinstance(layer, LayerH):
         n, ref = moe_hybrid_workspace_bytes(layer, T, k), layer.hot_ids
     elif isinstance(layer, Layer8):
@@ -127,7 +130,7 @@ def forward(layer, x, logits, k: int, out=None, ws=None, stream=None):
     """The layer on x for any expert format but MXFP4 (Layer: W4A8, Layer8: row-scaled FP8, Layer4: NVFP4, LayerH:
     hybrid).  LayerMX, for up to 16 tokens, is decode()'s."""
     import torch
-    _takes(layer, (Layer, Layer8, Layer4, LayerH), "forward")
+    _not_mxfp4(layer)
     if out is None:
         out = torch.empty_like(x)
     if ws is None:
@@ -215,7 +218,7 @@ def make_layer_mxfp4(gate_w, up_w, down_w, sh_gate=None, sh_up=None, sh_down=Non
 def alloc_decode_workspace(layer, T: int, k: int, device=None):
     """Scratch for decode / decode_router on a W4A8 or MXFP4 layer."""
     import torch
-    _takes(layer, (Layer, LayerMX), "decode")
+    _few_token(layer, "decode")
     if isinstance(layer, LayerMX):
         n, ref = moe_mxfp4_decode_workspace_bytes(layer, T, k), layer.gate_f4
     else:
@@ -231,7 +234,7 @@ def decode(layer, x, logits, k: int, out=None, ws=None, stream=None):
         with _on(stream):
             return decode(layer, x, logits, k, out, ws)
     import torch
-    _takes(layer, (Layer, LayerMX), "decode")
+    _few_token(layer, "decode")
     if out is None:
         out = torch.empty_like(x)
     if ws is None:
@@ -246,7 +249,7 @@ def decode_router(layer, x, wr, k: int, out=None, ws=None, stream=None):
         with _on(stream):
             return decode_router(layer, x, wr, k, out, ws)
     import torch
-    _takes(layer, (Layer, LayerMX), "decode_router")
+    _few_token(layer, "decode_router")
     if out is None:
         out = torch.empty_like(x)
     if ws is None:
